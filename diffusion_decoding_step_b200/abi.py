@@ -19,7 +19,8 @@ DLLM_W_BF16, DLLM_W_F32_SPLIT = 0, 1
 DLLM_COMMIT_THRESHOLD, DLLM_COMMIT_TOPK = 0, 1
 DLLM_DEVICE_TIMEOUT = 1  # status-word bit of a device wait that gave up
 DLLM_DEVICE_BAD_TOKEN = 2  # a token id outside [0, V) reached the embedding gather
-DLLM_DEVICE_INDEX = 4  # DLLM_DEBUG build: a row position from device memory was out of range
+DLLM_DEVICE_INDEX = 4  # a position or page id from device memory was out of range
+DLLM_KV_BF16, DLLM_KV_F16 = 0, 1
 
 
 class DllmError(RuntimeError):
@@ -47,11 +48,36 @@ class dllm_state(C.Structure):
                 ("tau", C.c_void_p)]
 
 
+class dllm_kv_pages(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64),
+                ("head_stride", C.c_int64), ("slot_stride", C.c_int64), ("n_pages", C.c_int32),
+                ("page_size", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("type", C.c_int32)]
+
+
+class dllm_rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("row_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class dllm_paged_batch(C.Structure):
+    _fields_ = [("n_seqs", C.c_int32), ("n_rows", C.c_int32), ("max_pages", C.c_int32),
+                ("table_stride", C.c_int32), ("row_start", C.c_void_p),
+                ("page_table", C.c_void_p)]
+
+
+class dllm_prefix_groups(C.Structure):
+    _fields_ = [("n_groups", C.c_int32), ("max_pages", C.c_int32), ("table_stride", C.c_int32),
+                ("seq_start", C.c_void_p), ("page_table", C.c_void_p), ("len", C.c_void_p)]
+
+
 _P = C.c_void_p
 _I = C.c_int32
 _CFG = C.POINTER(dllm_config)
 _W = C.POINTER(dllm_weights)
 _ST = C.POINTER(dllm_state)
+_KV = C.POINTER(dllm_kv_pages)
+_ROWS = C.POINTER(dllm_rows)
+_BT = C.POINTER(dllm_paged_batch)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -73,6 +99,14 @@ SIGNATURES = {
     "dllm_decode_block": (C.c_int, [_CFG, _W, _ST, _I, _I, C.POINTER(C.c_int32), _P,
                                     C.c_size_t, _P]),
     "dllm_decode_all": (C.c_int, [_CFG, _W, _ST, C.POINTER(C.c_int32), _P, C.c_size_t, _P]),
+    "dllm_paged_append": (C.c_int, [_KV, _BT, _I, _ROWS, _ROWS, _ROWS, _ROWS, _P, _P, C.c_float,
+                                    _P, _P]),
+    "dllm_paged_workspace_size": (C.c_int, [_KV, _I, _I, _I, C.POINTER(C.c_size_t)]),
+    "dllm_paged_workspace_init": (C.c_int, [_P, C.c_size_t, _P]),
+    "dllm_paged_attn": (C.c_int, [_KV, _BT, _I, _P, _P, C.c_float, _ROWS, _ROWS, _P, _P,
+                                  C.c_size_t, _P]),
+    "dllm_shared_prefix_attn": (C.c_int, [_KV, _BT, C.POINTER(dllm_prefix_groups), _I, _P, _P,
+                                          C.c_float, _ROWS, _ROWS, _P, _P, C.c_size_t, _P]),
     "dllm_step_outputs": (C.c_int, [_CFG, _P, C.c_size_t, C.POINTER(C.c_void_p),
                                     C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),
                                     C.POINTER(C.c_void_p), C.POINTER(C.c_void_p),

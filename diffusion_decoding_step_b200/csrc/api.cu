@@ -21,6 +21,7 @@
 namespace dllm {
 unsigned long long launch_count();
 void add_launches(long long n);
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 }
 
 using namespace dllm;
@@ -1144,6 +1145,8 @@ dllm_status refresh_graph(const Ctx& c, const dllm_config* cfg, const dllm_weigh
 }  // namespace
 
 // ====================================================================== C ABI
+PFN_cuTensorMapEncodeTiled_v12000 dllm::tensor_map_encoder() { return encode_fn(); }
+
 extern "C" {
 
 dllm_status dllm_workspace_size(const dllm_config* cfg, size_t* bytes) {

@@ -273,6 +273,54 @@ cudaError_t launch_rope_table(float2* tab, int S, int D, double theta, cudaStrea
 cudaError_t launch_split_f32(const float* src, __nv_bfloat16* dst, int64_t rows, int64_t cols,
                              cudaStream_t s);
 
+// ---------------------------------------------------------------- paged cache
+struct PagedPool {
+  void *k, *v;
+  long long page_stride, head_stride, slot_stride;  // elements
+  int n_pages, page_shift, Hkv, D, f16;
+};
+struct PagedRows {
+  void* data;
+  long long row_stride, head_stride;  // elements
+};
+struct PagedBatch {
+  int n_seqs, n_rows, max_pages, table_stride;
+  const int* row_start;
+  const int* table;
+};
+
+struct PagedAppendParams {
+  PagedPool kv;
+  PagedBatch bt;
+  int Hq;  // 0: no queries
+  PagedRows q, k, v, q_out;
+  const int* pos;
+  const int* shift;  // or null
+  int rope;          // 0: no rotation
+  int* status;       // or null
+  // turns (2 pi) per position of each pair, theta^(-2i/D) / (2 pi)
+  double turns[64];
+};
+cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
+
+struct PagedAttnParams {
+  PagedPool kv;
+  PagedBatch bt;
+  // shared prefixes (n_groups 0: none)
+  int n_groups, pmax_pages, ptable_stride;
+  const int* gseq;
+  const int* ptable;
+  const int* plen;
+  int Hq;
+  const int* segs;
+  const int* row_limit;  // or null
+  float scale_log2;
+  PagedRows q, out;
+  float* lse;  // or null
+  int* status;
+};
+cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t s);
+
 // Count of kernels launched by this library.
 void count_launch();
 

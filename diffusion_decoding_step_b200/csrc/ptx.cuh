@@ -11,7 +11,7 @@
 namespace dllm {
 
 // Error bits of the device status word.
-enum : int { kErrTimeout = 1, kErrBadArg = 2 };
+enum : int { kErrTimeout = 1, kErrBadArg = 2, kErrIndex = 4 };
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s

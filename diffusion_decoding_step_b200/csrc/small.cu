@@ -40,7 +40,6 @@ static cudaError_t launch_simple(K kern, dim3 grid, dim3 block, bool pdl, cudaSt
 // checks both what it reads and what it writes, so the projection and
 // attention kernels that read them later get checked values.  Other builds
 // compile the checks away.
-constexpr int kErrIndex = 4;  // status bit beside kErrTimeout and kErrBadArg
 #ifdef DLLM_DEBUG
 constexpr bool kDebugChecks = true;
 #else

@@ -1,0 +1,197 @@
+"""Paged key/value cache held in torch tensors, driven through the C ABI.
+
+PyTorch only allocates memory and provides the stream; the arithmetic runs in
+libdllm.so (``dllm_paged_append``, ``dllm_paged_attn``,
+``dllm_shared_prefix_attn``; include/dllm.h states what they compute).
+"""
+from __future__ import annotations
+
+import ctypes as C
+from typing import Optional
+
+import torch
+
+from . import abi
+
+_TYPES = {torch.bfloat16: abi.DLLM_KV_BF16, torch.float16: abi.DLLM_KV_F16}
+
+
+def _ints(t: torch.Tensor, what: str, shape: tuple, device) -> int:
+    """Address of a contiguous int32 tensor of the given shape (None: any size)."""
+    if t.dtype != torch.int32 or t.device != device or t.dim() != len(shape) \
+            or any(n is not None and n != m for n, m in zip(shape, t.shape)) \
+            or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous int32 tensor of shape "
+                         f"{['any' if n is None else n for n in shape]} on {device} is needed, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class PagedKV:
+    """Pages of keys and values, and the workspace of the attention over them.
+
+    ``k_pages`` / ``v_pages``: bf16 or fp16 [n_pages][Hkv][page_size][D] on one GPU, with
+    equal strides and contiguous D elements; other orders (slots before heads, keys and
+    values of a page side by side) are views.  ``max_rows`` bounds the rows of an attention
+    call, ``max_groups`` the prefix groups (0: ``shared_prefix_attn`` is not used).
+
+    Calls run on the current stream of the pages' device and return without waiting.  The
+    attention calls share one workspace: a PagedKV serves one of them at a time, and graphs or
+    streams that may overlap each take a PagedKV of their own over the same pages.
+    """
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, n_q_heads: int,
+                 max_rows: int, max_groups: int = 0):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape \
+                or k_pages.stride() != v_pages.stride() or k_pages.dtype != v_pages.dtype \
+                or k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages: two [n_pages][Hkv][page_size][D] tensors of one "
+                             "type, device and strides are needed")
+        if k_pages.dtype not in _TYPES:
+            raise ValueError(f"pages of {k_pages.dtype}: bfloat16 or float16 is needed")
+        if not k_pages.is_cuda:
+            raise ValueError("the pages have to be on a GPU")
+        if k_pages.stride(3) != 1:
+            raise ValueError("the D elements of a head have to be contiguous")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.device, self.dtype = k_pages.device, k_pages.dtype
+        n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_pages.shape
+        self.n_q_heads, self.max_rows, self.max_groups = n_q_heads, max_rows, max_groups
+        self._kv = abi.dllm_kv_pages(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.stride(0),
+                                     k_pages.stride(1), k_pages.stride(2), n_pages,
+                                     self.page_size, self.n_kv_heads, self.head_dim,
+                                     _TYPES[self.dtype])
+        self._kv_p = C.byref(self._kv)
+        n = C.c_size_t(0)
+        abi.check(abi.dllm_paged_workspace_size(self._kv_p, n_q_heads, max_rows, max_groups,
+                                                C.byref(n)), "paged_workspace_size")
+        self.ws_bytes = int(n.value)
+        with torch.cuda.device(self.device):
+            self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            self._ws_p = self.ws.data_ptr()
+            abi.check(abi.dllm_paged_workspace_init(self._ws_p, self.ws_bytes, self._stream()),
+                      "paged_workspace_init")
+
+    # ------------------------------------------------------------------ arguments
+    def _stream(self) -> int:
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def _call(self, what: str, fn, *args) -> None:
+        if torch.cuda.current_device() == self.device.index:
+            status = fn(*args, self._stream())
+        else:
+            with torch.cuda.device(self.device):
+                status = fn(*args, self._stream())
+        if status != abi.DLLM_OK:
+            abi.check(status, what)
+
+    def _rows(self, t: torch.Tensor, what: str, n_rows: Optional[int], heads: int):
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim \
+                or t.stride(2) != 1 or t.dtype != self.dtype or t.device != self.device \
+                or (n_rows is not None and t.shape[0] != n_rows):
+            raise ValueError(f"{what}: a {self.dtype} tensor [{n_rows or 'rows'}][{heads}]"
+                             f"[{self.head_dim}] on {self.device} with contiguous heads is needed, "
+                             f"got {t.dtype} {list(t.shape)} on {t.device}")
+        return C.byref(abi.dllm_rows(t.data_ptr(), t.stride(0), t.stride(1)))
+
+    def _batch(self, n_rows: int, row_start: torch.Tensor, page_table: torch.Tensor):
+        n = row_start.shape[0] - 1 if row_start.dim() == 1 else 0
+        if n < 1:
+            raise ValueError("row_start: an int32 tensor [n_seqs + 1] is needed")
+        rs = _ints(row_start, "row_start", (n + 1,), self.device)
+        tab = _ints(page_table, "page_table", (n, None), self.device)
+        width = page_table.shape[1]
+        return n, C.byref(abi.dllm_paged_batch(n, n_rows, width, width, rs, tab))
+
+    # ------------------------------------------------------------------ calls
+    def append(self, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
+               page_table: torch.Tensor, pos: torch.Tensor, q: Optional[torch.Tensor] = None,
+               q_out: Optional[torch.Tensor] = None, rope_theta: float = 0.0,
+               rope_shift: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+        """Append rows k, v [rows][Hkv][D] to the cache, k rotated; returns q [rows][Hq][D]
+        rotated (into q_out, which may be q), or None without q.
+
+        Rows [row_start[s], row_start[s+1]) go to positions pos[s].. of sequence s, rotated by
+        position + rope_shift[s]; page_table [n_seqs][pages] lists each sequence's pages."""
+        rows = k.shape[0]
+        n, bt = self._batch(rows, row_start, page_table)
+        heads = qp = qo = None
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            heads = self.n_q_heads
+            qp = self._rows(q, "q", rows, heads)
+            qo = self._rows(q_out, "q_out", rows, heads)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        self._call("paged_append", abi.lib().dllm_paged_append, self._kv_p, bt, heads or 0, qp,
+                   self._rows(k, "k", rows, self.n_kv_heads),
+                   self._rows(v, "v", rows, self.n_kv_heads), qo,
+                   _ints(pos, "pos", (n,), self.device),
+                   None if rope_shift is None else _ints(rope_shift, "rope_shift", (n,), self.device),
+                   rope_theta, self._ws_p)
+        return q_out
+
+    def _attn_args(self, q, row_start, page_table, segs, row_limit, out, lse):
+        rows = q.shape[0]
+        if rows > self.max_rows:
+            raise ValueError(f"{rows} rows: this PagedKV was made for {self.max_rows}")
+        n, bt = self._batch(rows, row_start, page_table)
+        if out is None:
+            out = torch.empty(rows, self.n_q_heads, self.head_dim, dtype=self.dtype,
+                              device=self.device)
+        lp = None
+        if lse is not None:
+            if lse.dtype != torch.float32 or lse.shape != (rows, self.n_q_heads) \
+                    or lse.device != self.device or not lse.is_contiguous():
+                raise ValueError(f"lse: a contiguous float32 tensor [{rows}][{self.n_q_heads}] on "
+                                 f"{self.device} is needed")
+            lp = lse.data_ptr()
+        return out, bt, (_ints(segs, "segs", (n, 2, 2), self.device),
+                         None if row_limit is None
+                         else _ints(row_limit, "row_limit", (rows,), self.device)), \
+            (self._rows(q, "q", rows, self.n_q_heads), self._rows(out, "out", rows, self.n_q_heads),
+             lp, self._ws_p, self.ws_bytes)
+
+    def attn(self, q: torch.Tensor, row_start: torch.Tensor, page_table: torch.Tensor,
+             segs: torch.Tensor, row_limit: Optional[torch.Tensor] = None, scale: float = 0.0,
+             out: Optional[torch.Tensor] = None,
+             lse: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Attention of rows q [rows][Hq][D] over the cache, into out (returned); lse, if given,
+        receives each row's log-sum-exp.
+
+        segs int32 [n_seqs][2][2]: (start, length) of the positions a sequence's rows see;
+        row_limit int32 [rows]: a row sees only positions below it.  Rows of no sequence are
+        left as they were (undefined in a fresh out)."""
+        out, bt, keys, rest = self._attn_args(q, row_start, page_table, segs, row_limit, out, lse)
+        self._call("paged_attn", abi.lib().dllm_paged_attn, self._kv_p, bt, self.n_q_heads, *keys,
+                   scale, *rest)
+        return out
+
+    def shared_prefix_attn(self, q: torch.Tensor, row_start: torch.Tensor,
+                           page_table: torch.Tensor, segs: torch.Tensor,
+                           group_start: torch.Tensor, prefix_table: torch.Tensor,
+                           prefix_len: torch.Tensor, row_limit: Optional[torch.Tensor] = None,
+                           scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                           lse: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """attn() for sequences that share prefixes: sequences [group_start[g],
+        group_start[g+1]) also see the prefix_len[g] positions of the pages in
+        prefix_table[g]."""
+        out, bt, keys, rest = self._attn_args(q, row_start, page_table, segs, row_limit, out, lse)
+        n = group_start.shape[0] - 1 if group_start.dim() == 1 else 0
+        if n < 1 or n > self.max_groups:
+            raise ValueError(f"{n} prefix groups: this PagedKV was made for 1 to {self.max_groups}")
+        width = prefix_table.shape[-1]
+        g = abi.dllm_prefix_groups(n, width, width,
+                                   _ints(group_start, "group_start", (n + 1,), self.device),
+                                   _ints(prefix_table, "prefix_table", (n, None), self.device),
+                                   _ints(prefix_len, "prefix_len", (n,), self.device))
+        self._call("shared_prefix_attn", abi.lib().dllm_shared_prefix_attn, self._kv_p, bt,
+                   C.byref(g), self.n_q_heads, *keys, scale, *rest)
+        return out
+
+    def device_status(self) -> int:
+        """The workspace's status word (waits for the current stream)."""
+        code = C.c_int32(0)
+        self._call("device_status", abi.lib().dllm_device_status, self._ws_p, C.byref(code))
+        return int(code.value)

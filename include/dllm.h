@@ -334,6 +334,124 @@ dllm_status dllm_decode_block(const dllm_config* cfg, const dllm_weights* w,
 dllm_status dllm_decode_all(const dllm_config* cfg, const dllm_weights* w, const dllm_state* st,
                             int32_t* passes, void* ws, size_t ws_bytes, dllm_stream stream);
 
+/* ------------------------------------------------------------------ paged cache
+ * A key/value cache in pages, for batches whose sequences differ in length or
+ * share pages.  No counterpart on the pages of the method; the operators
+ * stand beside dllm_qkv_proj (whose epilogue rotates q/k and writes the
+ * contiguous cache) and dllm_block_attn (which reads it).
+ *
+ * Rows.  A batch has n_seqs sequences; rows [row_start[s], row_start[s+1]) of
+ * the row buffers belong to sequence s (any number, none included; row_start
+ * is non-decreasing).  Rows before row_start[0] and behind row_start[n_seqs]
+ * (a padded batch) are neither read for a result nor written.
+ *
+ * Pages.  Position p of sequence s lives in slot p % page_size of page
+ * page_table[s*table_stride + p / page_size].  Sequences may share pages.
+ *
+ * Checked on the device, so that a launch can be captured and replayed with
+ * new contents: row_start, positions, segments and table entries may hold any
+ * value without an access out of bounds.  A table entry outside [0, n_pages)
+ * or a position outside the table that a call has to read or write sets
+ * DLLM_DEVICE_INDEX in the status word (in every build): an append then skips
+ * that row's keys and values, attention reads that page's keys and values as
+ * zeros, and leaves positions outside the table out.
+ *
+ * Supported: head_dim 32, 64 or 128; page_size a power of two in [8, 65536];
+ * n_q_heads a multiple of n_kv_heads, at most 128 query heads per kv head;
+ * n_seqs and n_groups <= 1024; n_rows < 2^24; max_pages * page_size <= 2^24.
+ * Data pointers must be 16-byte aligned and all strides multiples of 16 bytes
+ * (8 elements); the head_dim elements of a head are contiguous. */
+typedef enum { DLLM_KV_BF16 = 0, DLLM_KV_F16 = 1 } dllm_kv_type;
+
+typedef struct {
+  void* k;             /* element (page, head, slot, e) at k + page*page_stride +   */
+  void* v;             /* head*head_stride + slot*slot_stride + e; v likewise       */
+  int64_t page_stride, head_stride, slot_stride; /* in elements */
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+  int32_t type;        /* dllm_kv_type: of the pages and of every row buffer */
+} dllm_kv_pages;
+
+/* Row buffer: element (row, head, e) at data + row*row_stride + head*head_stride
+ * + e (in elements), so q, k and v may be slices of one packed projection. */
+typedef struct {
+  void* data;
+  int64_t row_stride, head_stride;
+} dllm_rows;
+
+typedef struct {
+  int32_t n_seqs, n_rows;     /* n_rows: rows of the row buffers */
+  int32_t max_pages;          /* entries of a table row that may be used */
+  int32_t table_stride;       /* entries from one table row to the next, >= max_pages */
+  const int32_t* row_start;   /* [n_seqs + 1] */
+  const int32_t* page_table;  /* [n_seqs][table_stride] */
+} dllm_paged_batch;
+
+/* Groups of consecutive sequences that share a prefix: group g holds sequences
+ * [seq_start[g], seq_start[g+1]); sequences outside every group have none. */
+typedef struct {
+  int32_t n_groups;
+  int32_t max_pages, table_stride;
+  const int32_t* seq_start;   /* [n_groups + 1], non-decreasing */
+  const int32_t* page_table;  /* [n_groups][table_stride] */
+  const int32_t* len;         /* [n_groups] prefix positions */
+} dllm_prefix_groups;
+
+/* Append rows to the cache, rotating q and k on the way.
+ * Row j of sequence s goes to position p = pos[s] + j; its rotary position is
+ * p + rope_shift[s] (rope_shift NULL: 0), the rotation is rotate-half RoPE
+ * with base rope_theta (0: none) as in dllm_qkv_proj, with the angle taken in
+ * 64 bits.  k [n_rows][n_kv_heads] rotated -> its slot, v -> its slot, and
+ * q [n_rows][n_q_heads] rotated -> q_out (q NULL: no queries, n_q_heads and
+ * q_out unused).  q_out may be q itself (same strides); otherwise no buffer may
+ * overlap another.  Slots that no row names keep their contents.  Two rows that
+ * name one slot (sequences that share the page they append to) leave a mixture
+ * of the two there.  status: device status word that receives
+ * DLLM_DEVICE_INDEX, or NULL. */
+dllm_status dllm_paged_append(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
+                              int32_t n_q_heads, const dllm_rows* q, const dllm_rows* k,
+                              const dllm_rows* v, const dllm_rows* q_out, const int32_t* pos,
+                              const int32_t* rope_shift, float rope_theta, int32_t* status,
+                              dllm_stream stream);
+
+/* Workspace bytes of the two attention calls below for batches of at most
+ * max_rows rows and n_q_heads query heads over these pages (host call);
+ * max_groups 0: dllm_paged_attn alone. */
+dllm_status dllm_paged_workspace_size(const dllm_kv_pages* kv, int32_t n_q_heads,
+                                      int32_t max_rows, int32_t max_groups, size_t* bytes);
+
+/* Clear the workspace's status word (256-byte aligned ws); once per workspace.
+ * dllm_device_status reads the word.  A workspace serves one call at a time. */
+dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream stream);
+
+/* Attention of a ragged batch of rows over the paged cache.
+ * Row r of sequence s sees the positions in the union of
+ * [segs[s][j][0], segs[s][j][0] + segs[s][j][1]), j = 0, 1 (device int32
+ * [n_seqs][2][2], as in dllm_block_attn), that are below row_limit[r] (device
+ * int32 [n_rows]; NULL: all).  So bidirectional blocks need no limit, and a
+ * causal or block-causal mask is a limit per row.  Query head h reads kv head
+ * h / (n_q_heads / n_kv_heads); scores are scaled by `scale` (0: 1/sqrt(D)).
+ * out[r][h] = softmax-weighted values; lse[r][h] (fp32 [n_rows][n_q_heads],
+ * NULL: not wanted) = the natural log of the sum of exponentials.  A row that
+ * sees nothing gets out = 0 and lse = -inf.  Slots outside every segment may
+ * hold anything, infinities and NaN included; inside the segments the values
+ * must be finite wherever any row of the sequence could read them.
+ * out must not overlap q. */
+dllm_status dllm_paged_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
+                            int32_t n_q_heads, const int32_t* segs, const int32_t* row_limit,
+                            float scale, const dllm_rows* q, const dllm_rows* out, float* lse,
+                            void* ws, size_t ws_bytes, dllm_stream stream);
+
+/* The same for a batch whose groups of sequences share a prefix: a row of
+ * group g also sees positions [0, len[g]) of the group's page list, whatever
+ * its row_limit, which counts the sequence's own positions.  The prefix is
+ * read and multiplied once per tile of the group's rows, not once per
+ * sequence. */
+dllm_status dllm_shared_prefix_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
+                                    const dllm_prefix_groups* groups, int32_t n_q_heads,
+                                    const int32_t* segs, const int32_t* row_limit, float scale,
+                                    const dllm_rows* q, const dllm_rows* out, float* lse,
+                                    void* ws, size_t ws_bytes, dllm_stream stream);
+
 /* Device pointers (into ws) of the last step's outputs: conf, tok, gap and
  * commit [b][B]; block_done and refresh_list [b], as dllm_threshold_commit
  * describes them.  Any output pointer may be NULL. */
@@ -350,7 +468,8 @@ dllm_status dllm_step_outputs(const dllm_config* cfg, void* ws, size_t ws_bytes,
  *  - DLLM_DEVICE_INDEX (4): only in the DLLM_DEBUG build (libdllm_debug.so,
  *    built by build.py --debug).  A row position read from device memory (a
  *    per-sequence block start) was outside the sequence, and the access was
- *    skipped.  The other builds do not check these positions. */
+ *    skipped.  The other builds do not check these positions.  The paged cache
+ *    calls set it in every build, as described there. */
 #define DLLM_DEVICE_BAD_TOKEN 2
 #define DLLM_DEVICE_INDEX 4
 dllm_status dllm_device_status(void* ws, int32_t* code, dllm_stream stream);
