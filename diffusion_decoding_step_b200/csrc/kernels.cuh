@@ -318,8 +318,21 @@ struct PagedAttnParams {
   PagedRows q, out;
   float* lse;  // or null
   int* status;
+  int G, rows_per_tile;  // query heads per kv head; rows of a query tile
+  // workspace: partial outputs of cut tiles [2 * kNumSMs][128][D] with their
+  // (max, sum) [2 * kNumSMs][128]; the cut tile that starts in a CTA
+  float* part;
+  float2* part_ml;
+  int4* cut;  // [kNumSMs] first row, rows, kv head, parts | slot parity << 16
+  // with groups: whole parts [own, prefix][n_rows][Hq][D] and where a row's
+  // parts are [own, prefix][n_rows][Hkv]
+  float* whole;
+  float2* whole_ml;
+  int2* where;
 };
-cudaError_t launch_paged_attn(const PagedAttnParams& p, cudaStream_t s);
+cudaError_t paged_attn_prepare();
+cudaError_t launch_paged_attn(const CUtensorMap& qmap, const CUtensorMap& kmap,
+                              const CUtensorMap& vmap, const PagedAttnParams& p, cudaStream_t s);
 
 // Count of kernels launched by this library.
 void count_launch();

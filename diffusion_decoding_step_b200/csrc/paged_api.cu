@@ -1,14 +1,20 @@
 // C-ABI entry points of the paged key/value cache: argument checks and
 // parameter blocks for the kernels in paged.cu.
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "../../include/dllm.h"
 #include "kernels.cuh"
+
+namespace dllm {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+}
 
 using namespace dllm;
 
@@ -80,7 +86,58 @@ dllm_status check_heads(int n_q_heads, const PagedPool& kv) {
   return DLLM_OK;
 }
 
-size_t workspace_bytes() { return 256; }
+// Workspace: status word, cut-tile records, partial outputs; with groups also
+// the whole parts and the row map.
+struct WsLayout {
+  size_t cut, part, part_ml, whole, whole_ml, where, total;
+};
+WsLayout ws_layout(const PagedPool& kv, int Hq, long long rows, bool groups) {
+  WsLayout l{};
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  l.cut = take(sizeof(int4) * kNumSMs);
+  l.part_ml = take(sizeof(float2) * 2 * kNumSMs * 128);
+  l.part = take(sizeof(float) * 2 * kNumSMs * 128 * kv.D);
+  if (groups) {
+    l.where = take(sizeof(int2) * 2 * rows * kv.Hkv);
+    l.whole_ml = take(sizeof(float2) * 2 * rows * Hq);
+    l.whole = take(sizeof(float) * 2 * rows * Hq * kv.D);
+  }
+  l.total = at;
+  return l;
+}
+
+// One-time per-device setup that must not run inside a stream capture.
+dllm_status prepare_device() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DLLM_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return DLLM_OK;
+  if (!tensor_map_encoder() || paged_attn_prepare() != cudaSuccess) return DLLM_ERR_CUDA;
+  done[dev] = true;
+  return DLLM_OK;
+}
+
+// Tensor map of 16-bit elements (any 16-bit type copies alike): extents d, byte
+// strides of axes 1.. where the extent is above one.
+bool make_map(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* d,
+              const long long* stride, const cuuint32_t* box, int head_dim) {
+  cuuint64_t st[3];
+  for (int i = 0; i + 1 < rank; ++i) st[i] = d[i + 1] > 1 ? 2 * (cuuint64_t)stride[i] : 256;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return tensor_map_encoder()(
+             m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), d, st, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             head_dim >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
                      const dllm_prefix_groups* groups, int32_t n_q_heads, const int32_t* segs,
@@ -114,14 +171,41 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
     p.plen = groups->len;
   }
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return DLLM_ERR_INVALID;
-  if (ws_bytes < workspace_bytes()) return DLLM_ERR_WORKSPACE;
+  const WsLayout l = ws_layout(p.kv, n_q_heads, p.bt.n_rows, groups != nullptr);
+  if (ws_bytes < l.total) return DLLM_ERR_WORKSPACE;
+  const int D = p.kv.D;
+  uint8_t* w = static_cast<uint8_t*>(ws);
   p.Hq = n_q_heads;
+  p.G = n_q_heads / p.kv.Hkv;
+  p.rows_per_tile = 128 / p.G;
   p.segs = segs;
   p.row_limit = row_limit;
-  p.scale_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.f / sqrtf((float)p.kv.D));
+  p.scale_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.f / sqrtf((float)D));
   p.lse = lse;
   p.status = static_cast<int*>(ws);
-  return launch_paged_attn(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  p.cut = reinterpret_cast<int4*>(w + l.cut);
+  p.part = reinterpret_cast<float*>(w + l.part);
+  p.part_ml = reinterpret_cast<float2*>(w + l.part_ml);
+  if (groups) {
+    p.whole = reinterpret_cast<float*>(w + l.whole);
+    p.whole_ml = reinterpret_cast<float2*>(w + l.whole_ml);
+    p.where = reinterpret_cast<int2*>(w + l.where);
+  }
+  e = prepare_device();
+  if (e != DLLM_OK) return e;
+  const cuuint32_t bd = D >= 64 ? 64 : D;
+  const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)n_q_heads, (cuuint64_t)p.bt.n_rows};
+  const long long qs[2] = {p.q.head_stride, p.q.row_stride};
+  const cuuint32_t qb[3] = {bd, (cuuint32_t)p.G, (cuuint32_t)p.rows_per_tile};
+  const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)kv->page_size, (cuuint64_t)p.kv.Hkv,
+                            (cuuint64_t)p.kv.n_pages};
+  const long long ks[3] = {p.kv.slot_stride, p.kv.head_stride, p.kv.page_stride};
+  const cuuint32_t kb[4] = {bd, (cuuint32_t)std::min(kv->page_size, 128), 1, 1};
+  CUtensorMap qm, km, vm;
+  if (!make_map(&qm, p.q.data, 3, qd, qs, qb, D) || !make_map(&km, p.kv.k, 4, kd, ks, kb, D) ||
+      !make_map(&vm, p.kv.v, 4, kd, ks, kb, D))
+    return DLLM_ERR_CUDA;
+  return launch_paged_attn(qm, km, vm, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? DLLM_OK
              : DLLM_ERR_CUDA;
 }
@@ -174,7 +258,7 @@ dllm_status dllm_paged_workspace_size(const dllm_kv_pages* kv, int32_t n_q_heads
   if (e != DLLM_OK) return e;
   if (!bytes || max_rows < 1 || max_groups < 0) return DLLM_ERR_INVALID;
   if (max_rows >= kMaxRows || max_groups > kMaxSeqs) return DLLM_ERR_UNSUPPORTED;
-  *bytes = workspace_bytes();
+  *bytes = ws_layout(pool, n_q_heads, max_rows, max_groups > 0).total;
   return DLLM_OK;
 }
 
