@@ -101,7 +101,7 @@ SIGNATURES = {
     "dllm_decode_all": (C.c_int, [_CFG, _W, _ST, C.POINTER(C.c_int32), _P, C.c_size_t, _P]),
     "dllm_paged_append": (C.c_int, [_KV, _BT, _I, _ROWS, _ROWS, _ROWS, _ROWS, _P, _P, C.c_float,
                                     _P, _P]),
-    "dllm_paged_workspace_size": (C.c_int, [_KV, _I, _I, _I, C.POINTER(C.c_size_t)]),
+    "dllm_paged_workspace_size": (C.c_int, [_KV, _I, _I, C.POINTER(C.c_size_t)]),
     "dllm_paged_workspace_init": (C.c_int, [_P, C.c_size_t, _P]),
     "dllm_paged_attn": (C.c_int, [_KV, _BT, _I, _P, _P, C.c_float, _ROWS, _ROWS, _P, _P,
                                   C.c_size_t, _P]),

@@ -319,20 +319,18 @@ struct PagedAttnParams {
   float* lse;  // or null
   int* status;
   int G, rows_per_tile;  // query heads per kv head; rows of a query tile
-  // workspace: partial outputs of cut tiles [2 * kNumSMs][128][D] with their
-  // (max, sum) [2 * kNumSMs][128]; the cut tile that starts in a CTA
+  // workspace: parts of cut query tiles, a CTA's two slots of slot_rows rows
+  // [2 * kNumSMs][slot_rows][D] with their (max, sum), and the cut tile that
+  // starts in a CTA [kNumSMs]: first row, rows, kv head, parts | slot parity << 16
+  int slot_rows;
   float* part;
   float2* part_ml;
-  int4* cut;  // [kNumSMs] first row, rows, kv head, parts | slot parity << 16
-  // with groups: whole parts [own, prefix][n_rows][Hq][D] and where a row's
-  // parts are [own, prefix][n_rows][Hkv]
-  float* whole;
-  float2* whole_ml;
-  int2* where;
+  int4* cut;
 };
 cudaError_t paged_attn_prepare();
 cudaError_t launch_paged_attn(const CUtensorMap& qmap, const CUtensorMap& kmap,
-                              const CUtensorMap& vmap, const PagedAttnParams& p, cudaStream_t s);
+                              const CUtensorMap& vmap, const PagedAttnParams& p, bool pair,
+                              cudaStream_t s);
 
 // Count of kernels launched by this library.
 void count_launch();

@@ -26,10 +26,14 @@ DLLM_DEV uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Rows [r0, r1) of sequence s, clamped to the row buffers whatever row_start holds.
-DLLM_DEV void seq_rows(const PagedBatch& bt, int s, int& r0, int& r1) {
-  r0 = min(max(bt.row_start[s], 0), bt.n_rows);
-  r1 = min(max(bt.row_start[s + 1], r0), bt.n_rows);
+// Visible range of (start, len) inside [0, cap); false if it reaches outside.
+DLLM_DEV bool clip_range(int st, int len, int cap, int& a, int& e) {
+  len = max(len, 0);
+  a = max(st, 0);
+  e = st < 0 ? min(st + len, cap) : a >= cap || len > cap - a ? cap : a + len;
+  const bool inside = len == 0 || (st >= 0 && a < cap && len <= cap - a);
+  if (len == 0 || e <= a) a = e = 0;
+  return inside;
 }
 
 // The two key segments of sequence s as disjoint ranges [a0, e0), [a1, e1)
@@ -39,31 +43,17 @@ struct Segs {
 };
 DLLM_DEV Segs seq_segs(const PagedAttnParams& p, int s) {
   const int* g = p.segs + 4 * (size_t)s;
-  const long long cap = (long long)p.bt.max_pages << p.kv.page_shift;
-  long long a[2], e[2];
-  bool cut = false;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const long long st = g[2 * j], len = g[2 * j + 1];
-    a[j] = max(st, 0ll);
-    e[j] = max(min(st + max(len, 0ll), cap), a[j]);
-    cut |= len > 0 && (st < 0 || st + len > cap);
-    if (len <= 0 || a[j] >= cap) a[j] = e[j] = 0;
+  const int s0 = g[0], l0 = g[1], s1 = g[2], l1 = g[3];
+  const int cap = p.bt.max_pages << p.kv.page_shift;
+  Segs r;
+  const bool in0 = clip_range(s0, l0, cap, r.a0, r.e0), in1 = clip_range(s1, l1, cap, r.a1, r.e1);
+  if (!(in0 && in1) && p.status != nullptr) atomicOr(p.status, kErrIndex);
+  if (r.a1 < r.e0 && r.a0 < r.e1) {  // they overlap: together one range
+    r.a0 = min(r.a0, r.a1);
+    r.e0 = max(r.e0, r.e1);
+    r.a1 = r.e1 = 0;
   }
-  if (cut && p.status != nullptr) atomicOr(p.status, kErrIndex);
-  if (a[0] < e[0] && a[1] < e[1]) {  // the part of the second that the first does not cover
-    if (a[1] >= a[0]) {
-      a[1] = max(a[1], e[0]);
-    } else if (e[1] <= e[0]) {
-      e[1] = min(e[1], a[0]);
-    } else {  // the second covers the first
-      a[0] = a[1];
-      e[0] = e[1];
-      a[1] = e[1] = 0;
-    }
-    if (a[1] >= e[1]) a[1] = e[1] = 0;
-  }
-  return Segs{(int)a[0], (int)e[0], (int)a[1], (int)e[1]};
+  return r;
 }
 
 }  // namespace
@@ -212,123 +202,102 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------ attention
-// Work.  An item is the own part of a sequence, or the prefix of a group: a
-// range of rows, and a list of 128-key tiles (aligned to 128 positions, so
-// that a tile is a whole number of pages or lies inside one).  The rows of an
-// item times the G query heads of a kv head are packed into tiles of 128
-// query rows, so a prefix is multiplied with the rows of all its sequences at
-// once.  All (item, kv head, query tile, key tile) units in this order form
-// one line that the CTAs (one per SM) cut into equal shares, whatever the
-// lengths on the device are: no host knowledge of them is needed, and the
-// shares of a ragged batch differ by one unit.  Every CTA finds its share
-// itself by a prefix sum over the items.
+// Work.  The rows of an item (a group of sequences that share a prefix, or a
+// sequence outside every group) times the G query heads of a kv head are
+// packed into query tiles, so that a prefix is multiplied with the rows of all
+// its sequences at once.  A query tile's keys are a list of 128-key tiles: the
+// prefix, then the own keys of each sequence that has rows in the tile, which
+// the other rows do not see.  Key tiles are aligned to 128 positions, so a tile
+// is a whole number of pages or lies inside one.
 //
-// A share is a list of pieces (a query tile and a run of key tiles).  Roles:
-//   warp 8      walks the share, describes each piece in a small queue, and
-//               loads Q, K and V tiles through TMA; each lane fetches its
-//               page's table entry and issues that page's boxes.  Pages that
-//               hold no key of the tile are requested past the last page, which
-//               TMA fills with zeros without reading.
+// All query tiles of all items and kv heads, each with its key tiles plus a
+// fixed cost, form one line that the CTAs (one per SM) cut into equal shares,
+// whatever the lengths on the device are.  Every CTA finds its share itself by
+// a prefix sum over the sequences, so the host needs no lengths and a captured
+// launch follows new ones.  A group's tiles are allotted their average length
+// on the line; a share of the allotment stands for the same share of the keys.
+//
+// A share is a list of pieces (a query tile and a run of its key tiles).  Roles:
+//   warp 8      walks the share, describes pieces and key tiles in two small
+//               queues, and loads Q, K and V through TMA; each lane fetches its
+//               page's table entry and issues that page's boxes.  Pages without
+//               a key of the tile are requested past the last page, which TMA
+//               fills with zeros without reading.
 //   warp 9      issues S = Q K^T and O += P V on tcgen05.
-//   warps 0-3   softmax of the even key tiles of a piece, warps 4-7 of the odd
-//               ones: two streams with their own S, P and O in TMEM, so that
-//               the products of one run during the softmax of the other.  A
-//               thread owns a query row; P overwrites S in TMEM as the A
-//               operand of the second product.  O is rescaled only when the
+//   warps 0-3 and 4-7   softmax of two streams with their own S, P and O in
+//               TMEM, so that the products of one run during the softmax of the
+//               other.  A thread owns a query row; P overwrites S in TMEM as the
+//               A operand of the second product.  O is rescaled only when the
 //               row's maximum grew by more than 2^8 (the kept maximum is then
 //               stale, which the final division cancels).
-// At the end of a piece the two streams' O are merged.  A tile that one CTA
-// did alone is written out; the parts of a cut tile go to the workspace in
-// fp32, and a second kernel merges them in a fixed order.
+// The streams are the even and odd key tiles of one 128-row query tile, merged
+// at the end of a piece, or (PAIR) the two halves of a 256-row query tile, which
+// then share every K and V tile.
+//
+// A query tile that one CTA did alone is written out.  The parts of a cut tile
+// go to the workspace in fp32, and a second kernel merges them in the order of
+// the keys.
 constexpr int kKeyTile = 128;
-constexpr int kAttnThreads = 320;
-constexpr int kMaxItems = 2048;
-constexpr int kQueue = 4;
+constexpr int kAttnThreads = 384;
+constexpr int kMaxSeqs = 1024;
+constexpr int kQueue = 4, kTileQueue = 8;
 constexpr float kGrow = 8.f;  // log2 of the growth of a maximum that rescales O
+constexpr int kTileCost = 2;  // fixed cost of a query tile, in key tiles
 
 struct Piece {
   int r0, nrows, kvh, n;        // first row, rows, kv head, key tiles (-1: no more pieces)
-  int kt0, kind;                // first key tile; 0 own part, 1 prefix
-  int a0, e0, a1, e1;           // key ranges
-  int dest;                     // kDestOut / kDestWhole / kDestPart
-  int slot;                     // partial slot
-  int where_x, where_y;         // row map entry to write, or where_x < 0
-  int pad0, pad1;
+  int parts;                    // parts of the query tile
+  int slot;                     // partial slot: 2 * CTA, + 1 where it is not the CTA's first piece
 };
-enum : int { kDestOut = 0, kDestWhole = 1, kDestPart = 2 };
-// Row map entry: x = dest | 4 if the row also has a prefix part | the row's
-// place in its query tile << 3; y = first slot | parts << 16.
 
-template <int D, int ST>
+template <int D, bool PAIR>
 struct PagedCfg {
+  static constexpr int kST = PAIR ? 4 : 5;  // K/V ring tiles
   static constexpr int kBoxD = D >= 64 ? 64 : D;
   static constexpr int kRowBytes = kBoxD * 2;
   static constexpr int kSw = kRowBytes == 128 ? 2 : 4;
   static constexpr int kNBox = D / kBoxD;
   static constexpr int kBoxBytes = 128 * kRowBytes;
   static constexpr int kTile = 128 * D * 2;  // bytes of a Q, K or V tile
-  static constexpr int kScan = (kMaxItems + 1) * 8;
-  static constexpr int kXBytes = 2 * 2 * 128 * 8;  // (max, sum) of both streams, two pieces
-  static constexpr size_t kSmem =
-      1024 + (1 + ST) * kTile + kScan + 8 + kXBytes + kQueue * sizeof(Piece) + 512;
+  static constexpr int kQ = PAIR ? 2 : 1;    // query tiles of 128 rows
+  // prefix sums of the units, row and group starts, group of each sequence
+  static constexpr int kPlan = 3 * (kMaxSeqs + 4) * 4 + kMaxSeqs * 2;
+  static constexpr int kX = 4096;  // (max, sum) of both streams, for two pieces
+  static constexpr size_t kSmem = 1024 + (kQ + kST) * kTile + kPlan + kX +
+                                  kQueue * sizeof(Piece) + kTileQueue * 16 + 512;
 };
 
-struct Item {
-  int r0, r1, kt, n0, tiles;
-  Segs sg;
-  const int* table;
-  int kind, seq;
-};
-
-DLLM_DEV int key_tiles(int a, int e) { return e > a ? (e + kKeyTile - 1) / kKeyTile - a / kKeyTile : 0; }
-
-DLLM_DEV Item load_item(const PagedAttnParams& p, int i) {
-  Item it;
-  if (i < p.n_groups) {
-    const int g0 = min(max(p.gseq[i], 0), p.bt.n_seqs);
-    const int g1 = min(max(p.gseq[i + 1], g0), p.bt.n_seqs);
-    it.r0 = min(max(p.bt.row_start[g0], 0), p.bt.n_rows);
-    it.r1 = min(max(p.bt.row_start[g1], it.r0), p.bt.n_rows);
-    const int cap = p.pmax_pages << p.kv.page_shift;
-    const int len = p.plen[i];
-    if (len > cap && p.status != nullptr) atomicOr(p.status, kErrIndex);
-    it.sg = Segs{0, min(max(len, 0), cap), 0, 0};
-    it.table = p.ptable + (size_t)i * p.ptable_stride;
-    it.kind = 1;
-    it.seq = -1;
-  } else {
-    const int s = i - p.n_groups;
-    seq_rows(p.bt, s, it.r0, it.r1);
-    it.sg = seq_segs(p, s);
-    it.table = p.bt.table + (size_t)s * p.bt.table_stride;
-    it.kind = 0;
-    it.seq = s;
-  }
-  it.n0 = key_tiles(it.sg.a0, it.sg.e0);
-  it.kt = it.n0 + key_tiles(it.sg.a1, it.sg.e1);
-  it.tiles = (it.r1 - it.r0 + p.rows_per_tile - 1) / p.rows_per_tile;
-  return it;
+DLLM_DEV int key_tiles(int a, int e) {
+  return e > a ? (e + kKeyTile - 1) / kKeyTile - a / kKeyTile : 0;
 }
-// Units of one query tile and kv head: its key tiles, and one for an own part
-// without keys, whose output has to be written all the same.
-DLLM_DEV int tile_units(const Item& it) { return it.kind ? it.kt : max(it.kt, 1); }
+DLLM_DEV int seg_tiles(const Segs& g) { return key_tiles(g.a0, g.e0) + key_tiles(g.a1, g.e1); }
 
 // First position and visible range [lo, hi) of key tile t of the ranges.
-DLLM_DEV void key_tile(int a0, int e0, int a1, int e1, int t, int& base, int& lo, int& hi) {
-  const int n0 = key_tiles(a0, e0);
-  const int a = t < n0 ? a0 : a1, e = t < n0 ? e0 : e1;
+DLLM_DEV void key_tile(const Segs& g, int t, int& base, int& lo, int& hi) {
+  const int n0 = key_tiles(g.a0, g.e0);
+  const int a = t < n0 ? g.a0 : g.a1, e = t < n0 ? g.e0 : g.e1;
   base = (a / kKeyTile + (t < n0 ? t : t - n0)) * kKeyTile;
   lo = max(a, base);
   hi = min(e, base + kKeyTile);
 }
 
-// Whether sequence s lies in a group with a prefix (whole warp).
-DLLM_DEV bool has_prefix(const PagedAttnParams& p, int s, int lane) {
-  bool in = false;
-  for (int g = lane; g < p.n_groups; g += 32)
-    in |= p.gseq[g] <= s && s < p.gseq[g + 1] && p.plen[g] > 0;
-  return __any_sync(0xffffffffu, in);
+DLLM_DEV int prefix_keys(const PagedAttnParams& p, int g) {
+  const int cap = p.pmax_pages << p.kv.page_shift;
+  const int len = p.plen[g];
+  if (len > cap && p.status != nullptr) atomicOr(p.status, kErrIndex);
+  return min(max(len, 0), cap);
 }
+
+// The line's shares: CTA c of G has units [start(c), start(c + 1)).
+struct Shares {
+  int each, rem;
+  DLLM_DEV int start(int c) const { return c * each + min(c, rem); }
+  DLLM_DEV int owner(int u) const {
+    const int big = rem * (each + 1);
+    return u < big ? (int)((unsigned)u / (unsigned)(each + 1))
+                   : rem + (int)((unsigned)(u - big) / (unsigned)each);
+  }
+};
 
 // A wait that ends when another role gave up; sets the flag when it gives up itself.
 DLLM_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
@@ -347,28 +316,51 @@ DLLM_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, int* status, volatil
   }
 }
 
-template <int D, bool F16, int ST>
+// Sum over the block's threads before this one (all threads; scratch of one
+// entry per warp).
+DLLM_DEV int block_before(int v, int* scratch, int warp, int lane) {
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  int before = inc - v;
+#pragma unroll
+  for (int w = 0; w < kAttnThreads / 32; ++w)
+    if (w < warp) before += scratch[w];
+  return before;
+}
+
+template <int D, bool F16, bool PAIR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ PagedAttnParams p) {
-  using C = PagedCfg<D, ST>;
+  using C = PagedCfg<D, PAIR>;
+  constexpr int ST = C::kST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
   uint8_t* q_s = base_s;
-  uint8_t* kv_s = q_s + C::kTile;  // [ST]
-  long long* upfx = reinterpret_cast<long long*>(kv_s + ST * C::kTile);  // [items + 1]
-  float2* x_s = reinterpret_cast<float2*>(upfx + kMaxItems + 2);         // [2][2][128]
-  Piece* queue = reinterpret_cast<Piece*>(x_s + 2 * 2 * 128);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(queue + kQueue);
-  uint64_t* kv_full = bars;             // [ST]
-  uint64_t* kv_empty = kv_full + ST;    // [ST]
-  uint64_t* d_full = kv_empty + ST;     // [kQueue]
-  uint64_t* d_empty = d_full + kQueue;  // [kQueue]
-  uint64_t* s_full = d_empty + kQueue;  // [2]
-  uint64_t* p_full = s_full + 2;        // [2]
+  uint8_t* kv_s = q_s + C::kQ * C::kTile;  // [ST]
+  int* upfx = reinterpret_cast<int*>(kv_s + ST * C::kTile);  // [n_seqs + 1]
+  int* rs = upfx + kMaxSeqs + 4;                             // [n_seqs + 1]
+  int* gs = rs + kMaxSeqs + 4;                               // [n_groups + 1]
+  short* gid = reinterpret_cast<short*>(gs + kMaxSeqs + 4);  // [n_seqs]
+  float* x_s = reinterpret_cast<float*>(gid + kMaxSeqs);
+  Piece* queue = reinterpret_cast<Piece*>(x_s + C::kX / 4);
+  int4* tiles_s = reinterpret_cast<int4*>(queue + kQueue);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(tiles_s + kTileQueue);  // [ST]
+  uint64_t* kv_empty = kv_full + ST;         // [ST]
+  uint64_t* d_full = kv_empty + ST;          // [kQueue]
+  uint64_t* d_empty = d_full + kQueue;       // [kQueue]
+  uint64_t* t_full = d_empty + kQueue;       // [kTileQueue]
+  uint64_t* s_full = t_full + kTileQueue;    // [2]
+  uint64_t* p_full = s_full + 2;             // [2]
   uint64_t* q_full = p_full + 2;
   uint64_t* q_empty = q_full + 1;
   uint64_t* o_full = q_empty + 1;
@@ -377,6 +369,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int tile_rows = p.rows_per_tile * C::kQ;
   if (t == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&kv_full[i], 1);
@@ -386,6 +379,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&d_full[i], 1);
       mbar_init(&d_empty[i], 257);
     }
+    for (int i = 0; i < kTileQueue; ++i) mbar_init(&t_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
@@ -403,195 +397,329 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp == 9) tmem_alloc(tmem_slot, 512);
   grid_dep_wait();
 
-  // ---- prefix sum of the items' units
-  const int n_items = p.n_groups + p.bt.n_seqs;
-  const int per = (n_items + kAttnThreads - 1) / kAttnThreads;
+  // ---- the line: row starts and groups (made non-decreasing, whatever they
+  // hold, so that all CTAs agree on disjoint items), then a prefix sum
+  const int n_seqs = p.bt.n_seqs;
+  constexpr int kPer = (kMaxSeqs + kAttnThreads - 1) / kAttnThreads;
+  const int per = (n_seqs + kAttnThreads - 1) / kAttnThreads;
   {
-    long long mine = 0;
-    for (int j = 0; j < per; ++j) {
-      const int i = t * per + j;
-      if (i >= n_items) break;
-      const Item it = load_item(p, i);
-      upfx[i + 1] = mine += (long long)it.tiles * p.kv.Hkv * tile_units(it);
-    }
-    long long inc = mine;
+    int kt[kPer];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    long long* sums = reinterpret_cast<long long*>(x_s);
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
-    long long before = inc - mine;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    for (int j = 0; j < per; ++j) {
+    for (int j = 0; j < kPer; ++j) {
       const int i = t * per + j;
-      if (i >= n_items) break;
-      upfx[i + 1] += before;
+      kt[j] = j < per && i < n_seqs ? seg_tiles(seq_segs(p, i)) : 0;
     }
-    if (t == 0) upfx[0] = 0;
+    for (int i = t; i <= n_seqs; i += kAttnThreads)
+      rs[i] = min(max(p.bt.row_start[i], 0), p.bt.n_rows);
+    if (p.n_groups > 0) {
+      for (int i = t; i <= p.n_groups; i += kAttnThreads) gs[i] = min(max(p.gseq[i], 0), n_seqs);
+      for (int i = t; i < n_seqs; i += kAttnThreads) gid[i] = -1;
+    }
+    __syncthreads();
+    bool bad = false;
+    for (int i = t; i < n_seqs; i += kAttnThreads) bad |= rs[i + 1] < rs[i];
+    for (int i = t; i < p.n_groups; i += kAttnThreads) bad |= gs[i + 1] < gs[i];
+    if (__syncthreads_or(bad)) {
+      if (t == 0) {
+        for (int i = 0; i < n_seqs; ++i) rs[i + 1] = max(rs[i + 1], rs[i]);
+        for (int i = 0; i < p.n_groups; ++i) gs[i + 1] = max(gs[i + 1], gs[i]);
+      }
+      __syncthreads();
+    }
+    int* scratch = reinterpret_cast<int*>(x_s);
+    int* opfx = reinterpret_cast<int*>(kv_s);  // own key tiles of earlier sequences
+    if (p.n_groups > 0) {
+      for (int g = t; g < p.n_groups; g += kAttnThreads)
+        if (prefix_keys(p, g) > 0)
+          for (int i = gs[g]; i < gs[g + 1]; ++i) gid[i] = (short)g;
+      int own[kPer], sum = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = t * per + j;
+        own[j] = 0;
+        if (j < per && i < n_seqs && rs[i + 1] > rs[i])
+          own[j] = kt[j] * ((rs[i + 1] - rs[i]) / tile_rows + 1);
+        sum += own[j];
+      }
+      int before = block_before(sum, scratch + 16, warp, lane);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = t * per + j;
+        if (j < per && i < n_seqs) {
+          opfx[i] = before;
+          before += own[j];
+          if (i == n_seqs - 1) opfx[n_seqs] = before;
+        }
+      }
+      __syncthreads();
+    }
+    int units[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = t * per + j;
+      units[j] = 0;
+      if (j < per && i < n_seqs) {
+        const int g = p.n_groups > 0 ? gid[i] : -1;
+        if (g < 0) {
+          const int nt = (rs[i + 1] - rs[i] + tile_rows - 1) / tile_rows;
+          units[j] = nt * p.kv.Hkv * (max(kt[j], 1) + kTileCost);
+        } else if (i == gs[g]) {
+          const int nt = (rs[gs[g + 1]] - rs[i] + tile_rows - 1) / tile_rows;
+          const int own = opfx[gs[g + 1]] - opfx[i];
+          if (nt > 0)
+            units[j] = nt * p.kv.Hkv *
+                       (key_tiles(0, prefix_keys(p, g)) + (own + nt - 1) / nt + kTileCost);
+        }
+      }
+      sum += units[j];
+    }
+    int before = block_before(sum, scratch, warp, lane);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = t * per + j;
+      if (j < per && i < n_seqs) {
+        upfx[i] = before;
+        before += units[j];
+        if (i == n_seqs - 1) upfx[n_seqs] = before;
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
-  const long long U = upfx[n_items];
-  const int G = (int)min((long long)gridDim.x, U);  // CTAs with work
-  const int cta = blockIdx.x;
 
   if (warp == 8) {
     // ================================================================ producer
-    long long u = 0, u1 = 0;
+    const int U = upfx[n_seqs];
+    const int G = min((int)gridDim.x, U);  // CTAs with work
+    const int cta = blockIdx.x;
+    Shares sh{0, 0};
+    int u = 0, u1 = 0;
     if (cta < G) {
-      u = (long long)cta * U / G;
-      u1 = (long long)(cta + 1) * U / G;
+      sh.each = (unsigned)U / (unsigned)G;
+      sh.rem = U - sh.each * G;
+      u = sh.start(cta);
+      u1 = sh.start(cta + 1);
     }
-    int lo = 0, hi = n_items;  // the last item that starts at or before u and has units
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
+    int4 cut = make_int4(0, 0, 0, 0);
+    int i = 0, hi = n_seqs;  // the last sequence that starts at or before u
+    while (hi - i > 1) {
+      const int mid = (i + hi) / 2;
       if (upfx[mid] <= u)
-        lo = mid;
+        i = mid;
       else
         hi = mid;
     }
-    int i = lo;
-    Item it{};
-    bool pfx = false;
-    if (u < u1) {
-      it = load_item(p, i);
-      pfx = it.kind == 0 && p.n_groups > 0 && has_prefix(p, it.seq, lane);
-    }
-    int4 cut = make_int4(0, 0, 0, 0);
-    int pos = 0, n_piece = 0, n_q = 0;  // ring position, pieces, pieces with keys
-    bool ok = true, first = true;
+    int pos = 0, n_piece = 0, n_q = 0, n_tile = 0;  // ring position; pieces, with keys; key tiles
+    bool ok = true, first_piece = true;
     const int page_boxes = max(1, kKeyTile >> p.kv.page_shift);
     const int slot_mask = (1 << p.kv.page_shift) - 1;
     const int page_keys = min(kKeyTile, slot_mask + 1);
     while (ok && u < u1) {
-      while (u >= upfx[i + 1]) {
-        ++i;
-        if (u < upfx[i + 1]) {
-          it = load_item(p, i);
-          pfx = it.kind == 0 && p.n_groups > 0 && has_prefix(p, it.seq, lane);
-        }
+      while (u >= upfx[i + 1]) ++i;
+      // ---- the query tile at u
+      const int g = p.n_groups > 0 ? gid[i] : -1;
+      const int seq_end = g >= 0 ? gs[g + 1] : i + 1;
+      const int item_r0 = rs[i], item_r1 = rs[seq_end];
+      const int nt = (item_r1 - item_r0 + tile_rows - 1) / tile_rows;
+      const int cost = (unsigned)(upfx[i + 1] - upfx[i]) / (unsigned)(nt * p.kv.Hkv);
+      const int tile = (unsigned)(u - upfx[i]) / (unsigned)cost;
+      const int start = upfx[i] + tile * cost, end = start + cost;
+      const int x0 = max(u, start + kTileCost), x1 = min(end, u1);
+      u = x1;
+      if (x1 <= x0) continue;
+      const int kvh = tile / nt;
+      const int r0 = item_r0 + (tile - kvh * nt) * tile_rows;
+      const int nrows = min(tile_rows, item_r1 - r0);
+      int sb = i;  // the sequence of the first row
+      for (int e = seq_end; e - sb > 1;) {
+        const int mid = (sb + e) / 2;
+        if (rs[mid] <= r0)
+          sb = mid;
+        else
+          e = mid;
       }
-      const int kt = tile_units(it);
-      const long long local = u - upfx[i];
-      const int tile = (int)(local / kt), k0 = (int)(local - (long long)tile * kt);
-      const int k1 = (int)min((long long)kt, k0 + (u1 - u));
-      const int kvh = tile / it.tiles, rt = tile - kvh * it.tiles;
-      const int r0 = it.r0 + rt * p.rows_per_tile;
-      const int nrows = min(p.rows_per_tile, it.r1 - r0);
-      int n = it.kt > 0 ? k1 - k0 : 0;
-      if (it.kind == 0 && p.row_limit != nullptr) {  // no row sees the last tiles
+      // 32 sequences at a time: each lane holds one's segments and key tiles
+      const int s_first = sb;
+      Segs sg{0, 0, 0, 0};
+      int kt = 0, incl = 0, own_before = 0;
+      auto load_chunk = [&]() {
+        const int s = sb + lane;
+        sg = Segs{0, 0, 0, 0};
+        if (s < seq_end && rs[s + 1] > max(rs[s], r0) && rs[s] < r0 + nrows) sg = seq_segs(p, s);
+        kt = seg_tiles(sg);
+        incl = kt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += x;
+        }
+      };
+      load_chunk();
+      int own_total = __shfl_sync(0xffffffffu, incl, 31);
+      if (p.row_limit != nullptr && rs[s_first + 1] >= r0 + nrows) {
+        // all rows of one sequence: its last tiles may be beyond every row's limit
         int lim = 0;
         for (int r = lane; r < nrows; r += 32) lim = max(lim, p.row_limit[r0 + r]);
         lim = __reduce_max_sync(0xffffffffu, lim);
-        while (n > 0) {
+        const Segs s0{__shfl_sync(0xffffffffu, sg.a0, 0), __shfl_sync(0xffffffffu, sg.e0, 0),
+                      __shfl_sync(0xffffffffu, sg.a1, 0), __shfl_sync(0xffffffffu, sg.e1, 0)};
+        while (own_total > 0) {
           int kb, kl, kh;
-          key_tile(it.sg.a0, it.sg.e0, it.sg.a1, it.sg.e1, k0 + n - 1, kb, kl, kh);
+          key_tile(s0, own_total - 1, kb, kl, kh);
           if (kl < lim) break;
-          --n;
+          --own_total;
         }
       }
-      const bool whole = k0 == 0 && k1 == kt;
-      const int slot = 2 * cta + (first ? 0 : 1);
-      int parts = 1;
-      if (!whole && k0 == 0) {  // the CTA of the tile's last unit
-        const long long last = upfx[i] + (long long)tile * kt + kt - 1;
-        parts = (int)(((last + 1) * G + U - 1) / U) - 1 - cta + 1;
-        cut = make_int4(r0, nrows, kvh, parts | (slot & 1) << 16);
+      while (sb + 32 < seq_end && rs[sb + 32] < r0 + nrows) {
+        sb += 32;
+        load_chunk();
+        own_total += __shfl_sync(0xffffffffu, incl, 31);
       }
+      if (sb != s_first) {
+        sb = s_first;
+        load_chunk();
+      }
+      const int ktp = g >= 0 ? key_tiles(0, prefix_keys(p, g)) : 0;
+      const int total = ktp + own_total, allot = cost - kTileCost;
+      int k0 = x0 - start - kTileCost, k1 = x1 - start - kTileCost;
+      if (total != allot) {
+        k0 = (int)((long long)k0 * total / allot);
+        k1 = (int)((long long)k1 * total / allot);
+      }
+      const int n = k1 - k0;
+
+      // ---- its description
       const int qi = n_piece % kQueue;
       if (lane == 0) {
         ok = n_piece < kQueue ||
              wait_or_abort(&d_empty[qi], (n_piece / kQueue - 1) & 1, p.status, abort);
         if (ok) {
-          Piece& d = queue[qi];
-          d.r0 = r0;
-          d.nrows = nrows;
-          d.kvh = kvh;
-          d.n = n;
-          d.kt0 = k0;
-          d.kind = it.kind;
-          d.a0 = it.sg.a0;
-          d.e0 = it.sg.e0;
-          d.a1 = it.sg.a1;
-          d.e1 = it.sg.e1;
-          d.dest = !whole ? kDestPart : (it.kind || pfx) ? kDestWhole : kDestOut;
-          d.slot = slot;
-          d.where_x = p.n_groups > 0 && k0 == 0 ? d.dest | (pfx ? 4 : 0) : -1;
-          d.where_y = slot | parts << 16;
+          Piece d{r0, nrows, kvh, n, 1, 2 * cta + (first_piece ? 0 : 1)};
+          if (x0 > start + kTileCost || x1 < end) {
+            d.parts = sh.owner(end - 1) - sh.owner(start + kTileCost) + 1;
+            if (x0 == start + kTileCost)
+              cut = make_int4(r0, nrows, kvh, d.parts | (d.slot & 1) << 16);
+          }
+          queue[qi] = d;
           mbar_arrive(&d_full[qi]);
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       ++n_piece;
-      first = false;
-      if (ok && n > 0) {
-        if (lane == 0) {
-          ok = n_q == 0 || wait_or_abort(q_empty, (n_q - 1) & 1, p.status, abort);
-          if (ok) {
-            mbar_arrive_expect_tx(q_full, C::kNBox * p.G * p.rows_per_tile * C::kRowBytes);
+      first_piece = false;
+      if (!ok || n == 0) continue;
+
+      // ---- its loads
+      if (lane == 0) {
+        ok = n_q == 0 || wait_or_abort(q_empty, (n_q - 1) & 1, p.status, abort);
+        if (ok) {
+          mbar_arrive_expect_tx(q_full,
+                                C::kQ * C::kNBox * p.G * p.rows_per_tile * C::kRowBytes);
+#pragma unroll
+          for (int h = 0; h < C::kQ; ++h)
 #pragma unroll
             for (int b = 0; b < C::kNBox; ++b)
-              tma_load_3d(q_s + b * C::kBoxBytes, &qmap, q_full, b * C::kBoxD, kvh * p.G, r0);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        ++n_q;
-        // this lane's page of key tile k0 + j (n_pages: nothing to read there)
-        auto entry = [&](int j) {
-          int page = p.kv.n_pages;
-          if (lane < page_boxes) {
-            int kb, kl, kh;
-            key_tile(it.sg.a0, it.sg.e0, it.sg.a1, it.sg.e1, k0 + j, kb, kl, kh);
-            const int at = kb + lane * page_keys;
-            if (at < kh && at + page_keys > kl) {
-              page = it.table[at >> p.kv.page_shift];
-              if (page < 0 || page >= p.kv.n_pages) {
-                if (p.status != nullptr) atomicOr(p.status, kErrIndex);
-                page = p.kv.n_pages;
-              }
-            }
-          }
-          return page;
-        };
-        auto load = [&](const CUtensorMap* m, int j, int page) {
-          const int st = pos % ST;
-          if (lane == 0) {
-            ok = pos < ST || wait_or_abort(&kv_empty[st], (pos / ST - 1) & 1, p.status, abort);
-            if (ok) mbar_arrive_expect_tx(&kv_full[st], C::kTile);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (ok) {
-            if (lane < page_boxes) {
-              int kb, kl, kh;
-              key_tile(it.sg.a0, it.sg.e0, it.sg.a1, it.sg.e1, k0 + j, kb, kl, kh);
-              uint8_t* dst = kv_s + st * C::kTile + lane * page_keys * C::kRowBytes;
-#pragma unroll
-              for (int b = 0; b < C::kNBox; ++b)
-                tma_load_4d(dst + b * C::kBoxBytes, m, &kv_full[st], b * C::kBoxD,
-                            page_keys == kKeyTile ? kb & slot_mask : 0, kvh, page);
-            }
-            ++pos;
-          }
-        };
-        // in the order the products take them: K0 K1 V0 K2 V1 ...
-        int e0 = entry(0), e1 = n > 1 ? entry(1) : 0;
-        if (ok) load(&kmap, 0, e0);
-        if (ok && n > 1) load(&kmap, 1, e1);
-        for (int j = 0; ok && j < n; ++j) {
-          const int e2 = j + 2 < n ? entry(j + 2) : 0;
-          load(&vmap, j, e0);
-          if (ok && j + 2 < n) load(&kmap, j + 2, e2);
-          e0 = e1;
-          e1 = e2;
+              tma_load_3d(q_s + h * C::kTile + b * C::kBoxBytes, &qmap, q_full, b * C::kBoxD,
+                          kvh * p.G, r0 + h * p.rows_per_tile);
         }
       }
-      u += k1 - k0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++n_q;
+      struct Loc {
+        int kb, kl, kh, w, page;
+      };
+      // key tile k of the list, and this lane's page of it (n_pages: nothing to read)
+      auto locate = [&](int k) {
+        Loc c;
+        Segs x{0, 0, 0, 0};
+        const int* table;
+        int kk = k;
+        if (k < ktp) {
+          x.e0 = prefix_keys(p, g);
+          table = p.ptable + (size_t)g * p.ptable_stride;
+          c.w = nrows << 9;
+        } else {
+          const int o = k - ktp;
+          while (o - own_before >= __shfl_sync(0xffffffffu, incl, 31) && sb + 32 < seq_end) {
+            own_before += __shfl_sync(0xffffffffu, incl, 31);
+            sb += 32;
+            load_chunk();
+          }
+          const int l = __ffs(__ballot_sync(0xffffffffu, incl > o - own_before)) - 1;
+          x = Segs{__shfl_sync(0xffffffffu, sg.a0, l), __shfl_sync(0xffffffffu, sg.e0, l),
+                   __shfl_sync(0xffffffffu, sg.a1, l), __shfl_sync(0xffffffffu, sg.e1, l)};
+          kk = o - own_before - __shfl_sync(0xffffffffu, incl - kt, l);
+          const int s = sb + l;
+          table = p.bt.table + (size_t)s * p.bt.table_stride;
+          c.w = max(rs[s] - r0, 0) | min(rs[s + 1] - r0, nrows) << 9 | 1 << 18;
+        }
+        key_tile(x, kk, c.kb, c.kl, c.kh);
+        c.page = p.kv.n_pages;
+        const int at = c.kb + lane * page_keys;
+        if (lane < page_boxes && at < c.kh && at + page_keys > c.kl) {
+          c.page = table[at >> p.kv.page_shift];
+          if (c.page < 0 || c.page >= p.kv.n_pages) {
+            if (p.status != nullptr) atomicOr(p.status, kErrIndex);
+            c.page = p.kv.n_pages;
+          }
+        }
+        return c;
+      };
+      auto load = [&](const CUtensorMap* m, const Loc& c) {
+        if (!ok) return;
+        const int st = pos % ST;
+        if (lane == 0) {
+          ok = pos < ST || wait_or_abort(&kv_empty[st], (pos / ST - 1) & 1, p.status, abort);
+          if (ok) mbar_arrive_expect_tx(&kv_full[st], C::kTile);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) return;
+        if (lane < page_boxes) {
+          uint8_t* dst = kv_s + st * C::kTile + lane * page_keys * C::kRowBytes;
+#pragma unroll
+          for (int b = 0; b < C::kNBox; ++b)
+            tma_load_4d(dst + b * C::kBoxBytes, m, &kv_full[st], b * C::kBoxD,
+                        page_keys == kKeyTile ? c.kb & slot_mask : 0, kvh, c.page);
+        }
+        ++pos;
+      };
+      // The description of a key tile goes with its K.  Its slot is free: the K
+      // ring is shorter than the queue, so the softmax is done with the tile
+      // that had the slot.
+      auto load_k = [&](const Loc& c) {
+        load(&kmap, c);
+        if (ok && lane == 0) {
+          tiles_s[n_tile % kTileQueue] = make_int4(c.kb, c.kl, c.kh, c.w);
+          mbar_arrive(&t_full[n_tile % kTileQueue]);
+        }
+        ++n_tile;
+      };
+      if constexpr (PAIR) {  // in the order the products take them: K0 V0 K1 V1 ...
+        Loc a = locate(k0);
+        for (int j = 0; ok && j < n; ++j) {
+          Loc b = a;
+          load_k(a);
+          if (j + 1 < n) b = locate(k0 + j + 1);
+          load(&vmap, a);
+          a = b;
+        }
+      } else {  // K0 K1 V0 K2 V1 ...
+        Loc a = locate(k0), b = a;
+        if (n > 1) b = locate(k0 + 1);
+        load_k(a);
+        if (n > 1) load_k(b);
+        for (int j = 0; ok && j < n; ++j) {
+          Loc c = b;
+          if (j + 2 < n) c = locate(k0 + j + 2);
+          load(&vmap, a);
+          if (j + 2 < n) load_k(c);
+          a = b;
+          b = c;
+        }
+      }
     }
     if (lane == 0) {
       const int qi = n_piece % kQueue;
@@ -600,7 +728,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         queue[qi].n = -1;
         mbar_arrive(&d_full[qi]);
       }
-      if (cta < kNumSMs) p.cut[cta] = cut;
+      p.cut[cta] = cut;
       if (*abort) {  // copies in flight land before the block goes
         for (int x = max(0, pos - ST); x < pos; ++x)
           mbar_wait(&kv_full[x % ST], (x / ST) & 1, p.status);
@@ -613,72 +741,88 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       constexpr uint32_t kIdS = idesc_16(F16, 128, kKeyTile, 0, 0);
       constexpr uint32_t kIdO = idesc_16(F16, 128, D, 0, 1);
       const uint32_t qa = smem_u32(q_s), kva = smem_u32(kv_s);
-      int pos = 0, n_piece = 0, n_q = 0;
-      int cnt[2] = {0, 0};  // P tiles taken of each stream
+      int base = 0, n_piece = 0, n_q = 0;  // ring position of the piece's first tile
+      int cnt[2] = {0, 0};                 // P tiles taken of each stream
       bool ok = true;
       while (ok) {
         const int qi = n_piece % kQueue;
         ok = wait_or_abort(&d_full[qi], (n_piece / kQueue) & 1, p.status, abort);
         if (!ok) break;
         const int n = queue[qi].n;
+        const bool two = PAIR && queue[qi].nrows > p.rows_per_tile;  // rows in both halves
         mbar_arrive(&d_empty[qi]);
         ++n_piece;
         if (n < 0) break;
         if (n == 0) continue;
-        auto wait_kv = [&]() {
-          return wait_or_abort(&kv_full[pos % ST], (pos / ST) & 1, p.status, abort);
+        auto k_pos = [&](int j) { return base + (PAIR ? 2 * j : j < 2 ? j : 2 * j - 1); };
+        auto v_pos = [&](int j) { return base + (PAIR ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1)); };
+        auto wait_kv = [&](int ps) {
+          return wait_or_abort(&kv_full[ps % ST], (ps / ST) & 1, p.status, abort);
         };
-        auto s_mma = [&](int j) {
-          if (!wait_kv()) return false;
+        // S of key tile j in stream x; the tile and Q are free after its last use
+        auto s_mma = [&](int x, int j, bool k_last) {
+          const int ps = k_pos(j);
+          if (!wait_kv(ps)) return false;
           tc_fence_after();
-          const uint32_t ka = kva + (pos % ST) * C::kTile;
-          const uint32_t d = tmem + (j & 1) * 128;
+          const uint32_t ka = kva + (ps % ST) * C::kTile;
+          const uint32_t qx = qa + (PAIR ? x * C::kTile : 0);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off =
                 (kk * 16 / C::kBoxD) * C::kBoxBytes + ((kk * 16) % C::kBoxD) * 2;
-            umma_bf16(d, smem_desc(qa + off, 16, 8 * C::kRowBytes, C::kSw),
+            umma_bf16(tmem + x * 128, smem_desc(qx + off, 16, 8 * C::kRowBytes, C::kSw),
                       smem_desc(ka + off, 16, 8 * C::kRowBytes, C::kSw), kIdS, kk > 0);
           }
-          umma_commit(&s_full[j & 1]);
-          umma_commit(&kv_empty[pos % ST]);
-          if (j == n - 1) umma_commit(q_empty);
-          ++pos;
+          umma_commit(&s_full[x]);
+          if (k_last) umma_commit(&kv_empty[ps % ST]);
+          if (k_last && j == n - 1) umma_commit(q_empty);
           return true;
         };
-        ok = wait_or_abort(q_full, n_q & 1, p.status, abort) && s_mma(0) && (n < 2 || s_mma(1));
-        for (int j = 0; ok && j < n; ++j) {
-          const int x = j & 1;
-          ok = wait_or_abort(&p_full[x], cnt[x] & 1, p.status, abort) &&
-               (j > 0 || n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort)) &&
-               wait_kv();
-          if (!ok) break;
+        auto pv_mma = [&](int x, int j, bool accumulate, bool v_last) {
+          const int ps = v_pos(j);
+          if (!wait_or_abort(&p_full[x], cnt[x] & 1, p.status, abort) || !wait_kv(ps))
+            return false;
           ++cnt[x];
           tc_fence_after();
-          const uint32_t va = kva + (pos % ST) * C::kTile;
+          const uint32_t va = kva + (ps % ST) * C::kTile;
 #pragma unroll
           for (int kk = 0; kk < kKeyTile / 16; ++kk)
             umma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8,
                         smem_desc(va + kk * 16 * C::kRowBytes, C::kBoxBytes, 8 * C::kRowBytes,
                                   C::kSw),
-                        kIdO, j > 1 || kk > 0);
-          umma_commit(&kv_empty[pos % ST]);
-          ++pos;
-          if (j + 2 < n) ok = s_mma(j + 2);
+                        kIdO, accumulate || kk > 0);
+          if (v_last) umma_commit(&kv_empty[ps % ST]);
+          return true;
+        };
+        ok = wait_or_abort(q_full, n_q & 1, p.status, abort);
+        if constexpr (PAIR) {
+          ok = ok && s_mma(0, 0, !two) && (!two || s_mma(1, 0, true));
+          ok = ok && (n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort));
+          for (int j = 0; ok && j < n; ++j) {
+            ok = pv_mma(0, j, j > 0, !two) && (j + 1 >= n || s_mma(0, j + 1, !two)) &&
+                 (!two || (pv_mma(1, j, j > 0, true) && (j + 1 >= n || s_mma(1, j + 1, true))));
+          }
+        } else {
+          ok = ok && s_mma(0, 0, true) && (n < 2 || s_mma(1, 1, true));
+          ok = ok && (n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort));
+          for (int j = 0; ok && j < n; ++j)
+            ok = pv_mma(j & 1, j, j > 1, true) && (j + 2 >= n || s_mma(j & 1, j + 2, true));
         }
         if (ok) umma_commit(o_full);
+        base += 2 * n;
         ++n_q;
       }
     }
-  } else {
+  } else if (warp < 8) {
     // ================================================================ softmax
     const int wg = warp >> 2, row = t & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_off + wg * 128;
     const uint32_t o_tm = tmem + lane_off + 256;
-    const int rr = row / p.G, hh = row - rr * p.G;
+    const int row_in = row / p.G, hh = row - row_in * p.G;
+    const int rr = row_in + (PAIR ? wg * p.rows_per_tile : 0);  // row within the query tile
     const int page_keys = min(kKeyTile, 1 << p.kv.page_shift);
-    int n_piece = 0, n_q = 0, s_cnt = 0, kv_base = 0;
+    int n_piece = 0, n_q = 0, s_cnt = 0, kv_base = 0, n_tile = 0;
     bool ok = true;
     while (ok) {
       const int qi = n_piece % kQueue;
@@ -688,78 +832,117 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_arrive(&d_empty[qi]);
       ++n_piece;
       if (d.n < 0) break;
-      const bool valid = rr < d.nrows && rr < p.rows_per_tile;
+      const bool valid = row_in < p.rows_per_tile && rr < d.nrows;
       const bool active = __any_sync(0xffffffffu, valid);
+      const bool stream = !PAIR || wg == 0 || d.nrows > p.rows_per_tile;  // the half has rows
       const int r = d.r0 + rr;
-      const int lim =
-          valid && d.kind == 0 && p.row_limit != nullptr ? p.row_limit[r] : INT_MAX;
+      const int limit = valid && p.row_limit != nullptr ? p.row_limit[r] : INT_MAX;
       float m = -FLT_MAX, l = 0.f;
-      for (int j = wg; j < d.n; j += 2) {
-        int kb, kl, kh;
-        key_tile(d.a0, d.e0, d.a1, d.e1, d.kt0 + j, kb, kl, kh);
+      const int j0 = PAIR ? 0 : wg;
+      for (int j = j0; stream && j < d.n; j += PAIR ? 1 : 2) {
+        const int ti = n_tile + j;
+        ok = wait_or_abort(&t_full[ti % kTileQueue], (ti / kTileQueue) & 1, p.status, abort);
+        if (!ok) break;
+        const int4 tl = tiles_s[ti % kTileQueue];  // base, lo, hi, rows
         ok = wait_or_abort(&s_full[wg], s_cnt & 1, p.status, abort);
         if (!ok) break;
         ++s_cnt;
         tc_fence_after();
-        if (active) {
-          float s[kKeyTile];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + c * 32, s + c * 32);
-          tmem_ld_wait();
-          const int first_k = kl - kb, end_k = min(kh, lim) - kb;
+        const bool own = tl.w >> 18;
+        const bool member = valid && rr >= (tl.w & 511) && rr < ((tl.w >> 9) & 511);
+        const int first_k = tl.y - tl.x;
+        const int end_k = member ? min(tl.z, own ? limit : INT_MAX) - tl.x : 0;
+        if (__any_sync(0xffffffffu, end_k > first_k)) {
+          // TMEM is read twice, for the maximum and for the probabilities, 32
+          // columns at a time: few registers and little code
           if (__any_sync(0xffffffffu, valid && (first_k > 0 || end_k < kKeyTile))) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float s[32];
+              tmem_ld32(s_tm + c * 32, s);
+              tmem_ld_wait32(s);
 #pragma unroll
-            for (int i = 0; i < kKeyTile; ++i)
-              if (i < first_k || i >= end_k) s[i] = -INFINITY;
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i < first_k || c * 32 + i >= end_k) s[i] = -INFINITY;
+              tmem_st32(s_tm + c * 32, reinterpret_cast<const uint32_t*>(s));
+            }
+            tmem_st_wait();
           }
           float mx[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float s[64];
+            tmem_ld32(s_tm + c * 64, s);
+            tmem_ld32(s_tm + c * 64 + 32, s + 32);
+            tmem_ld_wait32(s);
+            tmem_ld_wait32(s + 32);
 #pragma unroll
-          for (int i = 0; i < kKeyTile; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+            for (int i = 0; i < 64; i += 2)
+              mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(s[i], s[i + 1]));
+          }
           const float m_new =
               fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
-          if (j == wg) {
+          if (j == j0) {
             m = m_new;
           } else if (__any_sync(0xffffffffu, valid && m_new > m + kGrow)) {
             // S of this tile is complete, hence also the products before it
             const float alpha = fast_exp2(m - m_new);
             m = m_new;
             l *= alpha;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               float v[16];
               tmem_ld16(o_tm + wg * 128 + c * 16, v);
-              tmem_ld_wait();
+              tmem_ld_wait16(v);
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] *= alpha;
               tmem_st16(o_tm + wg * 128 + c * 16, v);
             }
           }
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          float s0[32], s1[32];
+          auto probs = [&](const float (&x)[32], int c) {
+            float pk[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float p0 = fast_exp2(fmaf(s[h * 64 + 2 * i], p.scale_log2, -m));
-              const float p1 = fast_exp2(fmaf(s[h * 64 + 2 * i + 1], p.scale_log2, -m));
+            for (int i = 0; i < 16; ++i) {
+              const float p0 = fast_exp2(fmaf(x[2 * i], p.scale_log2, -m));
+              const float p1 = fast_exp2(fmaf(x[2 * i + 1], p.scale_log2, -m));
               ls[i & 3] += p0 + p1;
-              pk[i] = pack2<F16>(p0, p1);
+              pk[i] = __uint_as_float(pack2<F16>(p0, p1));
             }
-            tmem_st32(s_tm + h * 32, pk);
+            tmem_st16(s_tm + c * 16, pk);  // below the columns that are still to be read
+          };
+          tmem_ld32(s_tm, s0);
+          tmem_ld_wait32(s0);
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tmem_ld32(s_tm + c * 32 + 32, s1);
+            probs(s0, c);
+            tmem_ld_wait32(s1);
+            if (c == 0) tmem_ld32(s_tm + 64, s0);
+            probs(s1, c + 1);
+            tmem_ld_wait32(s0);
           }
           l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          tmem_st_wait();
+        } else if (active) {  // no row of this warp sees the tile
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) pk[i] = 0u;
+          tmem_st32(s_tm, pk);
+          tmem_st32(s_tm + 32, pk);
           tmem_st_wait();
         }
         // Slots of a loaded page outside the tile's range may hold anything,
         // infinities and NaN included: their weight is zero, their values have
         // to be as well.
-        if (kl > kb || kh < kb + kKeyTile) {
-          const int vp = kv_base + min(2 * j + 2, 2 * d.n - 1);
-          const int key = kb + row;
+        if (tl.y > tl.x || tl.z < tl.x + kKeyTile) {
+          const int vp = kv_base + (PAIR ? 2 * j + 1 : min(2 * j + 2, 2 * d.n - 1));
+          const int key = tl.x + row;
           const int pg = key & ~(page_keys - 1);
           ok = wait_or_abort(&kv_full[vp % ST], (vp / ST) & 1, p.status, abort);
           if (!ok) break;
-          if ((key < kl || key >= kh) && pg < kh && pg + page_keys > kl) {
+          if ((key < tl.y || key >= tl.z) && pg < tl.z && pg + page_keys > tl.y) {
             uint4* v = reinterpret_cast<uint4*>(kv_s + (vp % ST) * C::kTile + row * C::kRowBytes);
 #pragma unroll
             for (int b = 0; b < C::kNBox; ++b)
@@ -773,69 +956,79 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_arrive(&p_full[wg]);
       }
       if (!ok) break;
-      // ---- the piece's result: (max, sum) of both streams, then each group of
-      // warps takes one half of the columns
-      float a0 = 0.f, a1 = 0.f, mt = -FLT_MAX, lt = 0.f;
+      n_tile += d.n;
+      kv_base += 2 * d.n;
+      // ---- the piece's result
+      float a0 = 1.f, a1 = 0.f, mt = m, lt = l;
       if (d.n > 0) {
-        float2* x = x_s + (n_q & 1) * 256;
-        x[wg * 128 + row] = make_float2(m, l);
-        named_bar_sync(1, 256);
-        const float2 y0 = x[row], y1 = x[128 + row];
-        mt = fmaxf(y0.x, y1.x);
-        a0 = fast_exp2(y0.x - mt);
-        a1 = d.n > 1 ? fast_exp2(y1.x - mt) : 0.f;
-        lt = y0.y * a0 + (d.n > 1 ? y1.y * a1 : 0.f);
-        kv_base += 2 * d.n;
+        if constexpr (!PAIR) {  // (max, sum) of both streams; each takes half of the columns
+          float2* x = reinterpret_cast<float2*>(x_s) + (n_q & 1) * 256;
+          x[wg * 128 + row] = make_float2(m, l);
+          named_bar_sync(1, 256);
+          const float2 y0 = x[row], y1 = x[128 + row];
+          mt = fmaxf(y0.x, y1.x);
+          a0 = fast_exp2(y0.x - mt);
+          a1 = d.n > 1 ? fast_exp2(y1.x - mt) : 0.f;
+          lt = y0.y * a0 + (d.n > 1 ? y1.y * a1 : 0.f);
+        }
         ok = wait_or_abort(o_full, n_q & 1, p.status, abort);
         if (!ok) break;
         ++n_q;
         tc_fence_after();
       }
-      constexpr int kCols = D / 2;
-      const int c0 = wg * kCols;
+      constexpr int kCols = PAIR ? D : D / 2;
+      constexpr int kC = kCols < 32 ? kCols : 32;
+      const int c0 = PAIR ? 0 : wg * kCols;
       const int head = d.kvh * p.G + hh;
+      const size_t part_row = (size_t)d.slot * p.slot_rows + (PAIR ? wg * 128 : 0) + row;
       if (active) {
-        if (d.dest == kDestOut) {
+        if (d.parts == 1) {
           const float inv = lt > 0.f ? 1.f / lt : 0.f;
           a0 *= inv;
           a1 *= inv;
         }
         uint16_t* out = static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride +
                         head * p.out.head_stride + c0;
-        float* part =
-            d.dest == kDestPart
-                ? p.part + ((size_t)d.slot * 128 + row) * D + c0
-                : p.whole + (((size_t)d.kind * p.bt.n_rows + r) * p.Hq + head) * D + c0;
-#pragma unroll
-        for (int c = 0; c < kCols / 16; ++c) {
-          float v[16];
+        float* part = p.part + part_row * D + c0;
+#pragma unroll 1
+        for (int c = 0; c < kCols / kC; ++c) {
+          float v[kC], w[kC];
           if (d.n > 0) {
-            tmem_ld16(o_tm + c0 + c * 16, v);
-            tmem_ld_wait();
+            const uint32_t at = o_tm + (PAIR ? wg * 128 : 0) + c0 + c * kC;
+            if constexpr (kC == 32) {
+              tmem_ld32(at, v);
+              if (!PAIR && d.n > 1) tmem_ld32(at + 128, w);
+            } else {
+              tmem_ld16(at, reinterpret_cast<float(&)[16]>(v));
+              if (!PAIR && d.n > 1) tmem_ld16(at + 128, reinterpret_cast<float(&)[16]>(w));
+            }
+            if constexpr (kC == 32) {
+              tmem_ld_wait32(v);
+              if (!PAIR && d.n > 1) tmem_ld_wait32(w);
+            } else {
+              tmem_ld_wait16(v);
+              if (!PAIR && d.n > 1) tmem_ld_wait16(w);
+            }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= a0;
-            if (d.n > 1) {
-              float w[16];
-              tmem_ld16(o_tm + 128 + c0 + c * 16, w);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = fmaf(w[i], a1, v[i]);
+            for (int i = 0; i < kC; ++i) {
+              v[i] *= a0;
+              if (!PAIR && d.n > 1) v[i] = fmaf(w[i], a1, v[i]);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.f;
+            for (int i = 0; i < kC; ++i) v[i] = 0.f;
           }
           if (valid) {
-            if (d.dest == kDestOut) {
+            if (d.parts == 1) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 8)
-                *reinterpret_cast<uint4*>(out + c * 16 + i) =
+              for (int i = 0; i < kC; i += 8)
+                *reinterpret_cast<uint4*>(out + c * kC + i) =
                     make_uint4(pack2<F16>(v[i], v[i + 1]), pack2<F16>(v[i + 2], v[i + 3]),
                                pack2<F16>(v[i + 4], v[i + 5]), pack2<F16>(v[i + 6], v[i + 7]));
-            } else {
+            } else if (lt > 0.f) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(part + c * 16 + i) =
+              for (int i = 0; i < kC; i += 4)
+                *reinterpret_cast<float4*>(part + c * kC + i) =
                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
           }
@@ -845,19 +1038,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tc_fence_before();
         mbar_arrive(o_empty);
       }
-      if (valid && wg == 0) {
-        if (d.dest == kDestOut) {
-          if (p.lse != nullptr)
-            p.lse[(size_t)r * p.Hq + head] =
-                lt > 0.f ? 0.6931471805599453f * mt + logf(lt) : -INFINITY;
-        } else if (d.dest == kDestPart) {
-          p.part_ml[d.slot * 128 + row] = make_float2(mt, lt);
-        } else {
-          p.whole_ml[((size_t)d.kind * p.bt.n_rows + r) * p.Hq + head] = make_float2(mt, lt);
-        }
-        if (d.where_x >= 0 && hh == 0)
-          p.where[((size_t)d.kind * p.bt.n_rows + r) * p.kv.Hkv + d.kvh] =
-              make_int2(d.where_x | (rr * p.G) << 3, d.where_y);
+      if (valid && (PAIR || wg == 0)) {
+        if (d.parts > 1)
+          p.part_ml[part_row] = make_float2(mt, lt);
+        else if (p.lse != nullptr)
+          p.lse[(size_t)r * p.Hq + head] =
+              lt > 0.f ? 0.6931471805599453f * mt + logf(lt) : -INFINITY;
       }
     }
   }
@@ -870,8 +1056,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------ merges
-// Lane i of a warp holds D / 32 neighbouring elements of a row.
+// ------------------------------------------------------------------ merge
+// Block (c, y) merges rows y, y + kMergeY, ... of the cut query tile that starts
+// in CTA c of the attention kernel: its parts are in that CTA's slot and in the
+// even slots of the CTAs after it.  A warp takes a row, lane i D / 32 of its
+// elements; where the block has fewer rows than warps, several warps share the
+// parts of a row.
+constexpr int kMergeWarps = 8, kMergeY = 16;
+
 template <int D>
 struct RowSum {
   static constexpr int kE = D / 32;
@@ -880,17 +1072,8 @@ struct RowSum {
 #pragma unroll
     for (int i = 0; i < kE; ++i) o[i] = 0.f;
   }
-  DLLM_DEV void add(float2 ml, const float* part, int lane) {
-    float v[kE];
-    if constexpr (kE == 4)
-      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(part + 4 * lane);
-    else if constexpr (kE == 2)
-      *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(part + 2 * lane);
-    else
-      v[0] = part[lane];
-    join(ml, v);
-  }
   DLLM_DEV void join(float2 ml, const float* v) {
+    if (ml.y == 0.f) return;  // a part without keys, whose elements are not written
     const float mn = fmaxf(m, ml.x);
     const float a = fast_exp2(m - mn), b = fast_exp2(ml.x - mn);
     m = mn;
@@ -899,128 +1082,112 @@ struct RowSum {
     for (int i = 0; i < kE; ++i) o[i] = o[i] * a + v[i] * b;
   }
 };
-
-template <int D, bool F16>
-DLLM_DEV void write_row(const PagedAttnParams& p, const RowSum<D>& s, int r, int head, int lane) {
-  constexpr int kE = RowSum<D>::kE;
-  const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
-  uint16_t* out =
-      static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride + head * p.out.head_stride;
-  if constexpr (kE == 1) {
-    out[lane] = (uint16_t)pack2<F16>(s.o[0] * inv, 0.f);
-  } else {
-    uint32_t w[kE / 2];
-#pragma unroll
-    for (int i = 0; i < kE / 2; ++i) w[i] = pack2<F16>(s.o[2 * i] * inv, s.o[2 * i + 1] * inv);
-    if constexpr (kE == 4)
-      *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(out + 2 * lane) = w[0];
-  }
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[(size_t)r * p.Hq + head] =
-        s.l > 0.f ? 0.6931471805599453f * s.m + logf(s.l) : -INFINITY;
+template <int N>
+DLLM_DEV void load_n(float* v, const float* src) {
+  if constexpr (N == 4)
+    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+  else if constexpr (N == 2)
+    *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+  else
+    v[0] = *src;
 }
-
-// Without groups: block (c, y) merges rows y, y + kMergeY, ... of the cut tile
-// that starts in CTA c of the attention kernel; its parts are in that CTA's
-// slot and in the first slots of the CTAs after it.  The block's warps share
-// the parts of a row, in a fixed order.
-constexpr int kMergeWarps = 8, kMergeY = 8;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kMergeWarps * 32)
-    paged_merge_cut_kernel(const __grid_constant__ PagedAttnParams p) {
+    paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int kE = RowSum<D>::kE;
   __shared__ float2 ml_s[kMergeWarps];
   __shared__ float o_s[kMergeWarps][D];
   grid_dep_wait();
   grid_dep_launch();
-  const int4 c = p.cut[blockIdx.x];
-  const int parts = c.w & 0xffff;
-  if (parts < 2) return;
-  const int slot0 = 2 * blockIdx.x + (c.w >> 16);
+  const int4 cut = p.cut[blockIdx.x];  // first row, rows, kv head, parts | slot parity << 16
+  const int parts = cut.w & 0xffff, slot0 = 2 * blockIdx.x + (cut.w >> 16);
+  const int rows = cut.y * p.G;
+  if (parts < 2 || (int)blockIdx.y >= rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int x = blockIdx.y; x < c.y * p.G; x += kMergeY) {
-    RowSum<D> s;
-    for (int i = warp; i < parts; i += kMergeWarps) {
-      const size_t at = (size_t)(i == 0 ? slot0 : 2 * (blockIdx.x + i)) * 128 + x;
-      s.add(p.part_ml[at], p.part + at * D, lane);
-    }
-    if (lane == 0) ml_s[warp] = make_float2(s.m, s.l);
+  const int here = (rows - blockIdx.y + kMergeY - 1) / kMergeY;  // rows of this block
+  const int split = here > 4 ? 1 : here > 2 ? 2 : here > 1 ? 4 : 8;
+  const int wrow = warp / split, wpart = warp - wrow * split;
+  for (int k0 = 0; k0 < here; k0 += kMergeWarps / split) {
+    const int z = (k0 + wrow) * kMergeY + blockIdx.y;
+    const bool have = k0 + wrow < here;
+    const int zr = z / p.G, zh = z - zr * p.G;
+    const int half = zr / p.rows_per_tile;  // 256-row tiles: 128 slots for each half
+    const int at = half * 128 + (zr - half * p.rows_per_tile) * p.G + zh;
+    RowSum<D> sum;
+    if (have) {
+      constexpr int kUn = 4;
+      for (int i = wpart; i < parts; i += kUn * split) {
+        float2 ml[kUn];
+        float v[kUn][kE];
 #pragma unroll
-    for (int i = 0; i < kE; ++i) o_s[warp][lane * kE + i] = s.o[i];
-    __syncthreads();
-    if (warp == 0) {
-      for (int w = 1; w < kMergeWarps; ++w) s.join(ml_s[w], &o_s[w][lane * kE]);
-      const int rr = x / p.G;
-      write_row<D, F16>(p, s, c.x + rr, c.z * p.G + x - rr * p.G, lane);
-    }
-    __syncthreads();
-  }
-}
-
-// With groups: one warp per (row, query head) merges its own part and its
-// prefix part, each whole or cut.  Rows of no sequence, and rows that the
-// attention kernel wrote itself, are left alone.
-template <int D, bool F16>
-__global__ void __launch_bounds__(kMergeWarps * 32)
-    paged_merge_rows_kernel(const __grid_constant__ PagedAttnParams p) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const long long id = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const int r = (int)(id / p.Hq), head = (int)(id - (long long)r * p.Hq);
-  if (r >= p.bt.n_rows || r < p.bt.row_start[0] || r >= p.bt.row_start[p.bt.n_seqs]) return;
-  const int kvh = head / p.G;
-  const int2 own = p.where[(size_t)r * p.kv.Hkv + kvh];
-  if ((own.x & 3) == kDestOut) return;
-  RowSum<D> s;
-  for (int kind = 0; kind < ((own.x & 4) ? 2 : 1); ++kind) {
-    const size_t row = (size_t)kind * p.bt.n_rows + r;
-    const int2 w = kind ? p.where[row * p.kv.Hkv + kvh] : own;
-    if ((w.x & 3) == kDestWhole) {
-      const size_t at = row * p.Hq + head;
-      s.add(p.whole_ml[at], p.whole + at * D, lane);
-    } else if ((w.x & 3) == kDestPart) {
-      // bounded whatever the entry holds: a row that a decreasing row_start
-      // leaves without a tile has an old one
-      const int c0 = min((w.y & 0xffff) >> 1, kNumSMs - 1), slot0 = 2 * c0 + (w.y & 1);
-      const int parts = min(w.y >> 16, kNumSMs - c0);
-      const int x = min(((w.x >> 3) & 127) + head - kvh * p.G, 127);
-      for (int i = 0; i < parts; ++i) {
-        const size_t at = (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * 128 + x;
-        s.add(p.part_ml[at], p.part + at * D, lane);
+        for (int k = 0; k < kUn; ++k) {
+          const int ip = i + k * split;
+          ml[k] = make_float2(-FLT_MAX, 0.f);
+          if (ip < parts) {
+            const size_t ro = (size_t)(ip == 0 ? slot0 : 2 * (blockIdx.x + ip)) * p.slot_rows + at;
+            ml[k] = p.part_ml[ro];
+            load_n<kE>(v[k], p.part + ro * D + lane * kE);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kUn; ++k) sum.join(ml[k], v[k]);
       }
     }
+    if (split > 1) {
+      if (lane == 0) ml_s[warp] = make_float2(sum.m, sum.l);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) o_s[warp][lane * kE + i] = sum.o[i];
+      __syncthreads();
+      if (wpart == 0)
+        for (int w = warp + 1; w < warp + split; ++w) sum.join(ml_s[w], &o_s[w][lane * kE]);
+      __syncthreads();
+    }
+    if (have && wpart == 0) {
+      const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
+      const int r = cut.x + zr, head = cut.z * p.G + zh;
+      uint16_t* out =
+          static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride + head * p.out.head_stride;
+      if constexpr (kE == 4)
+        *reinterpret_cast<uint2*>(out + 4 * lane) =
+            make_uint2(pack2<F16>(sum.o[0] * inv, sum.o[1] * inv),
+                       pack2<F16>(sum.o[2] * inv, sum.o[3] * inv));
+      else if constexpr (kE == 2)
+        *reinterpret_cast<uint32_t*>(out + 2 * lane) =
+            pack2<F16>(sum.o[0] * inv, sum.o[1] * inv);
+      else
+        out[lane] = (uint16_t)pack2<F16>(sum.o[0] * inv, 0.f);
+      if (lane == 0 && p.lse != nullptr)
+        p.lse[(size_t)r * p.Hq + head] =
+            sum.l > 0.f ? 0.6931471805599453f * sum.m + logf(sum.l) : -INFINITY;
+    }
   }
-  write_row<D, F16>(p, s, r, head, lane);
 }
 
 namespace {
 
-constexpr int kStages = 5;
-
 template <int D, bool F16>
 cudaError_t launch_paged_attn_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
-                                const PagedAttnParams& p, cudaStream_t s) {
-  const cudaError_t e =
-      launch_pdl(paged_attn_kernel<D, F16, kStages>, dim3(kNumSMs), dim3(kAttnThreads),
-                 PagedCfg<D, kStages>::kSmem, s, qm, km, vm, p);
+                                const PagedAttnParams& p, bool pair, cudaStream_t s) {
+  const dim3 grid(kNumSMs), block(kAttnThreads);
+  const cudaError_t e = pair ? launch_pdl(paged_attn_kernel<D, F16, true>, grid, block,
+                                          PagedCfg<D, true>::kSmem, s, qm, km, vm, p)
+                             : launch_pdl(paged_attn_kernel<D, F16, false>, grid, block,
+                                          PagedCfg<D, false>::kSmem, s, qm, km, vm, p);
   if (e != cudaSuccess) return e;
-  const dim3 block(kMergeWarps * 32);
-  if (p.n_groups == 0)
-    return launch_pdl(paged_merge_cut_kernel<D, F16>, dim3(kNumSMs, kMergeY), block, 0, s, p);
-  const long long warps = (long long)p.bt.n_rows * p.Hq;
-  return launch_pdl(paged_merge_rows_kernel<D, F16>,
-                    dim3((unsigned)((warps + kMergeWarps - 1) / kMergeWarps)), block, 0, s, p);
+  return launch_pdl(paged_merge_kernel<D, F16>, dim3(kNumSMs, kMergeY), dim3(kMergeWarps * 32), 0,
+                    s, p);
 }
 
 template <int D, bool F16>
 cudaError_t prepare_t() {
-  return cudaFuncSetAttribute(paged_attn_kernel<D, F16, kStages>,
+  const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, F16, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)PagedCfg<D, false>::kSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(paged_attn_kernel<D, F16, true>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)PagedCfg<D, kStages>::kSmem);
+                              (int)PagedCfg<D, true>::kSmem);
 }
 
 }  // namespace
@@ -1036,15 +1203,15 @@ cudaError_t paged_attn_prepare() {
 }
 
 cudaError_t launch_paged_attn(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
-                              const PagedAttnParams& p, cudaStream_t s) {
+                              const PagedAttnParams& p, bool pair, cudaStream_t s) {
   const int D = p.kv.D;
   if (p.kv.f16)
-    return D == 128  ? launch_paged_attn_t<128, true>(qm, km, vm, p, s)
-           : D == 64 ? launch_paged_attn_t<64, true>(qm, km, vm, p, s)
-                     : launch_paged_attn_t<32, true>(qm, km, vm, p, s);
-  return D == 128  ? launch_paged_attn_t<128, false>(qm, km, vm, p, s)
-         : D == 64 ? launch_paged_attn_t<64, false>(qm, km, vm, p, s)
-                   : launch_paged_attn_t<32, false>(qm, km, vm, p, s);
+    return D == 128  ? launch_paged_attn_t<128, true>(qm, km, vm, p, pair, s)
+           : D == 64 ? launch_paged_attn_t<64, true>(qm, km, vm, p, pair, s)
+                     : launch_paged_attn_t<32, true>(qm, km, vm, p, pair, s);
+  return D == 128  ? launch_paged_attn_t<128, false>(qm, km, vm, p, pair, s)
+         : D == 64 ? launch_paged_attn_t<64, false>(qm, km, vm, p, pair, s)
+                   : launch_paged_attn_t<32, false>(qm, km, vm, p, pair, s);
 }
 
 }  // namespace dllm

@@ -86,29 +86,21 @@ dllm_status check_heads(int n_q_heads, const PagedPool& kv) {
   return DLLM_OK;
 }
 
-// Workspace: status word, cut-tile records, partial outputs; with groups also
-// the whole parts and the row map.
-struct WsLayout {
-  size_t cut, part, part_ml, whole, whole_ml, where, total;
-};
-WsLayout ws_layout(const PagedPool& kv, int Hq, long long rows, bool groups) {
-  WsLayout l{};
-  size_t at = 256;
-  auto take = [&](size_t bytes) {
-    const size_t o = at;
-    at += (bytes + 255) / 256 * 256;
-    return o;
-  };
-  l.cut = take(sizeof(int4) * kNumSMs);
-  l.part_ml = take(sizeof(float2) * 2 * kNumSMs * 128);
-  l.part = take(sizeof(float) * 2 * kNumSMs * 128 * kv.D);
-  if (groups) {
-    l.where = take(sizeof(int2) * 2 * rows * kv.Hkv);
-    l.whole_ml = take(sizeof(float2) * 2 * rows * Hq);
-    l.whole = take(sizeof(float) * 2 * rows * Hq * kv.D);
-  }
-  l.total = at;
-  return l;
+// Query tiles of 256 rows share every key tile between two halves; they are
+// taken when an item (a group, or a sequence without one) has more than 128
+// query rows on average.
+bool pair_tiles(long long n_rows, int items, int G) { return n_rows * G > 128ll * items; }
+
+// Workspace: status word, a record per CTA, the parts of cut query tiles.
+constexpr size_t kWsCut = 256, kWsParts = 4096;
+static_assert(kWsCut + sizeof(int4) * kNumSMs <= kWsParts, "the records fit before the parts");
+
+int slot_rows(long long n_rows, int G) {
+  const long long rows = n_rows * G;
+  return rows > 128 ? 256 : (int)((rows + 7) / 8 * 8);
+}
+size_t workspace_bytes(const PagedPool& kv, int slot) {
+  return kWsParts + (size_t)2 * kNumSMs * slot * (kv.D * sizeof(float) + sizeof(float2));
 }
 
 // One-time per-device setup that must not run inside a stream capture.
@@ -171,26 +163,29 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
     p.plen = groups->len;
   }
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return DLLM_ERR_INVALID;
-  const WsLayout l = ws_layout(p.kv, n_q_heads, p.bt.n_rows, groups != nullptr);
-  if (ws_bytes < l.total) return DLLM_ERR_WORKSPACE;
-  const int D = p.kv.D;
-  uint8_t* w = static_cast<uint8_t*>(ws);
+  // The line of work units (key tiles, and a cost per query tile) has 32-bit
+  // coordinates: its length at the tables' full width has to fit.
+  const int g128 = 128 / (n_q_heads / p.kv.Hkv);
+  const long long own_tiles = (((long long)p.bt.max_pages << p.kv.page_shift) + 127) / 128;
+  const long long pre_tiles = (((long long)p.pmax_pages << p.kv.page_shift) + 127) / 128;
+  const long long q_tiles = p.bt.n_rows / g128 + p.bt.n_seqs;
+  if (q_tiles * p.kv.Hkv * (2 * own_tiles + pre_tiles + 8) >= (1ll << 31))
+    return DLLM_ERR_UNSUPPORTED;
   p.Hq = n_q_heads;
   p.G = n_q_heads / p.kv.Hkv;
+  p.slot_rows = slot_rows(p.bt.n_rows, p.G);
+  if (ws_bytes < workspace_bytes(p.kv, p.slot_rows)) return DLLM_ERR_WORKSPACE;
+  const int D = p.kv.D;
+  uint8_t* w = static_cast<uint8_t*>(ws);
   p.rows_per_tile = 128 / p.G;
   p.segs = segs;
   p.row_limit = row_limit;
   p.scale_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.f / sqrtf((float)D));
   p.lse = lse;
   p.status = static_cast<int*>(ws);
-  p.cut = reinterpret_cast<int4*>(w + l.cut);
-  p.part = reinterpret_cast<float*>(w + l.part);
-  p.part_ml = reinterpret_cast<float2*>(w + l.part_ml);
-  if (groups) {
-    p.whole = reinterpret_cast<float*>(w + l.whole);
-    p.whole_ml = reinterpret_cast<float2*>(w + l.whole_ml);
-    p.where = reinterpret_cast<int2*>(w + l.where);
-  }
+  p.cut = reinterpret_cast<int4*>(w + kWsCut);
+  p.part = reinterpret_cast<float*>(w + kWsParts);
+  p.part_ml = reinterpret_cast<float2*>(p.part + (size_t)2 * kNumSMs * p.slot_rows * D);
   e = prepare_device();
   if (e != DLLM_OK) return e;
   const cuuint32_t bd = D >= 64 ? 64 : D;
@@ -205,7 +200,9 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
   if (!make_map(&qm, p.q.data, 3, qd, qs, qb, D) || !make_map(&km, p.kv.k, 4, kd, ks, kb, D) ||
       !make_map(&vm, p.kv.v, 4, kd, ks, kb, D))
     return DLLM_ERR_CUDA;
-  return launch_paged_attn(qm, km, vm, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  const bool pair = pair_tiles(p.bt.n_rows, groups ? p.n_groups : p.bt.n_seqs, p.G);
+  return launch_paged_attn(qm, km, vm, p, pair, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
              ? DLLM_OK
              : DLLM_ERR_CUDA;
 }
@@ -251,20 +248,20 @@ dllm_status dllm_paged_append(const dllm_kv_pages* kv, const dllm_paged_batch* b
 }
 
 dllm_status dllm_paged_workspace_size(const dllm_kv_pages* kv, int32_t n_q_heads,
-                                      int32_t max_rows, int32_t max_groups, size_t* bytes) {
+                                      int32_t max_rows, size_t* bytes) {
   PagedPool pool;
   dllm_status e = check_shape(kv, &pool);
   if (e == DLLM_OK) e = check_heads(n_q_heads, pool);
   if (e != DLLM_OK) return e;
-  if (!bytes || max_rows < 1 || max_groups < 0) return DLLM_ERR_INVALID;
-  if (max_rows >= kMaxRows || max_groups > kMaxSeqs) return DLLM_ERR_UNSUPPORTED;
-  *bytes = ws_layout(pool, n_q_heads, max_rows, max_groups > 0).total;
+  if (!bytes || max_rows < 1) return DLLM_ERR_INVALID;
+  if (max_rows >= kMaxRows) return DLLM_ERR_UNSUPPORTED;
+  *bytes = workspace_bytes(pool, slot_rows(max_rows, n_q_heads / pool.Hkv));
   return DLLM_OK;
 }
 
 dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream stream) {
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return DLLM_ERR_INVALID;
-  if (ws_bytes < 256) return DLLM_ERR_WORKSPACE;
+  if (ws_bytes < kWsParts) return DLLM_ERR_WORKSPACE;
   return cudaMemsetAsync(ws, 0, 256, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? DLLM_OK
              : DLLM_ERR_CUDA;

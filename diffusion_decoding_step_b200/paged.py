@@ -63,8 +63,7 @@ class PagedKV:
                                      _TYPES[self.dtype])
         self._kv_p = C.byref(self._kv)
         n = C.c_size_t(0)
-        abi.check(abi.dllm_paged_workspace_size(self._kv_p, n_q_heads, max_rows, max_groups,
-                                                C.byref(n)), "paged_workspace_size")
+        abi.check(abi.dllm_paged_workspace_size(self._kv_p, n_q_heads, max_rows, C.byref(n)), "paged_workspace_size")
         self.ws_bytes = int(n.value)
         with torch.cuda.device(self.device):
             self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)

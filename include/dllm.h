@@ -358,7 +358,10 @@ dllm_status dllm_decode_all(const dllm_config* cfg, const dllm_weights* w, const
  *
  * Supported: head_dim 32, 64 or 128; page_size a power of two in [8, 65536];
  * n_q_heads a multiple of n_kv_heads, at most 128 query heads per kv head;
- * n_seqs and n_groups <= 1024; n_rows < 2^24; max_pages * page_size <= 2^24.
+ * n_seqs and n_groups <= 1024; n_rows < 2^24; max_pages * page_size <= 2^24;
+ * for attention, 128-row query tiles times 128-position key tiles times kv heads
+ * at the tables' full width (about (n_rows * n_q_heads / 128 + n_seqs *
+ * n_kv_heads) * max_pages * page_size / 64) < 2^31.
  * Data pointers must be 16-byte aligned and all strides multiples of 16 bytes
  * (8 elements); the head_dim elements of a head are contiguous. */
 typedef enum { DLLM_KV_BF16 = 0, DLLM_KV_F16 = 1 } dllm_kv_type;
@@ -414,10 +417,9 @@ dllm_status dllm_paged_append(const dllm_kv_pages* kv, const dllm_paged_batch* b
                               dllm_stream stream);
 
 /* Workspace bytes of the two attention calls below for batches of at most
- * max_rows rows and n_q_heads query heads over these pages (host call);
- * max_groups 0: dllm_paged_attn alone. */
+ * max_rows rows and n_q_heads query heads over these pages (host call). */
 dllm_status dllm_paged_workspace_size(const dllm_kv_pages* kv, int32_t n_q_heads,
-                                      int32_t max_rows, int32_t max_groups, size_t* bytes);
+                                      int32_t max_rows, size_t* bytes);
 
 /* Clear the workspace's status word (256-byte aligned ws); once per workspace.
  * dllm_device_status reads the word.  A workspace serves one call at a time. */

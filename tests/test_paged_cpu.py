@@ -46,17 +46,15 @@ def groups(**kw):
     return C.byref(abi.dllm_prefix_groups(**a))
 
 
-def size(kv, hq=28, n=5, g=0):
+def size(kv, hq=28, n=5):
     out = C.c_size_t(0)
-    return abi.dllm_paged_workspace_size(kv, hq, n, g, C.byref(out)), out.value
+    return abi.dllm_paged_workspace_size(kv, hq, n, C.byref(out)), out.value
 
 
 def test_workspace_size(lib):
-    st, plain = size(pages())
-    assert st == OK and plain >= 256
-    st, grouped = size(pages(), g=3)
-    assert st == OK and grouped >= plain
-    assert size(pages(), n=2000, g=3)[1] >= grouped
+    st, least = size(pages())
+    assert st == OK and least >= 4096
+    assert size(pages(), n=2000)[1] >= size(pages(), n=18)[1] >= least
     assert size(pages(head_dim=96))[0] == UNSUPPORTED
     assert size(pages(page_size=48))[0] == UNSUPPORTED
     assert size(pages(page_size=4))[0] == UNSUPPORTED
@@ -69,13 +67,11 @@ def test_workspace_size(lib):
     assert size(pages(n_kv_heads=1), hq=129)[0] == UNSUPPORTED
     assert size(pages(), n=0)[0] == INVALID
     assert size(pages(), n=1 << 24)[0] == UNSUPPORTED
-    assert size(pages(), g=-1)[0] == INVALID
-    assert size(pages(), g=1025)[0] == UNSUPPORTED
     assert size(None)[0] == INVALID
-    assert abi.dllm_paged_workspace_size(pages(), 28, 5, 0, None) == INVALID
+    assert abi.dllm_paged_workspace_size(pages(), 28, 5, None) == INVALID
     assert abi.dllm_paged_workspace_init(None, 256, None) == INVALID
     assert abi.dllm_paged_workspace_init(D0 + 8, 256, None) == INVALID
-    assert abi.dllm_paged_workspace_init(D0, 255, None) == WORKSPACE
+    assert abi.dllm_paged_workspace_init(D0, 4095, None) == WORKSPACE
 
 
 BAD_POOL = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(k=D0 + 8), INVALID),
@@ -125,13 +121,12 @@ def test_append_refusals(lib):
 def test_attention_refusals(lib):
     no_gpu()
     n = size(pages())[1]
-    ng = size(pages(), g=1)[1]
 
     def both(want, kv=None, bt=None, hq=28, segs=D0, lim=None, scale=0.0, q=None, out=None, lse=None,
              ws=D0, short=0):
         kv, bt, q, out = kv or pages(), bt or batch(), q or rows(), out or rows(data=2 * D0)
         assert abi.dllm_paged_attn(kv, bt, hq, segs, lim, scale, q, out, lse, ws, n - short, None) == want
-        assert abi.dllm_shared_prefix_attn(kv, bt, groups(), hq, segs, lim, scale, q, out, lse, ws, ng - short,
+        assert abi.dllm_shared_prefix_attn(kv, bt, groups(), hq, segs, lim, scale, q, out, lse, ws, n - short,
                                            None) == want
 
     for kw, want in BAD_POOL:
@@ -155,9 +150,9 @@ def test_attention_refusals(lib):
                      (dict(table_stride=3), INVALID), (dict(seq_start=None), INVALID), (dict(len=D0 + 2), INVALID),
                      (dict(page_table=None), INVALID), (dict(max_pages=1 << 19, table_stride=1 << 19), UNSUPPORTED)]:
         assert abi.dllm_shared_prefix_attn(pages(), batch(), groups(**kw), 28, D0, None, 0.0, rows(),
-                                           rows(data=2 * D0), None, D0, ng, None) == want, kw
+                                           rows(data=2 * D0), None, D0, n, None) == want, kw
     assert abi.dllm_shared_prefix_attn(pages(), batch(), None, 28, D0, None, 0.0, rows(), rows(data=2 * D0), None,
-                                       D0, ng, None) == INVALID
+                                       D0, n, None) == INVALID
 
 
 def test_paged_kv_wants_gpu_pages(lib):
