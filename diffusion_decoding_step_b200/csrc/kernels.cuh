@@ -327,9 +327,11 @@ struct PagedAttnParams {
   float2* part_ml;
   int4* cut;
 };
+// Query tiles of 128 rows, of 256 rows, of 32 rows (paged.cu says how they work).
+enum PagedMode : int { kPagedSplit = 0, kPagedPair = 1, kPagedQuad = 2 };
 cudaError_t paged_attn_prepare();
 cudaError_t launch_paged_attn(const CUtensorMap& qmap, const CUtensorMap& kmap,
-                              const CUtensorMap& vmap, const PagedAttnParams& p, bool pair,
+                              const CUtensorMap& vmap, const PagedAttnParams& p, int mode,
                               cudaStream_t s);
 
 // Count of kernels launched by this library.

@@ -41,9 +41,7 @@ DLLM_DEV bool clip_range(int st, int len, int cap, int& a, int& e) {
 struct Segs {
   int a0, e0, a1, e1;
 };
-DLLM_DEV Segs seq_segs(const PagedAttnParams& p, int s) {
-  const int* g = p.segs + 4 * (size_t)s;
-  const int s0 = g[0], l0 = g[1], s1 = g[2], l1 = g[3];
+DLLM_DEV Segs make_segs(const PagedAttnParams& p, int s0, int l0, int s1, int l1) {
   const int cap = p.bt.max_pages << p.kv.page_shift;
   Segs r;
   const bool in0 = clip_range(s0, l0, cap, r.a0, r.e0), in1 = clip_range(s1, l1, cap, r.a1, r.e1);
@@ -54,6 +52,10 @@ DLLM_DEV Segs seq_segs(const PagedAttnParams& p, int s) {
     r.a1 = r.e1 = 0;
   }
   return r;
+}
+DLLM_DEV Segs seq_segs(const PagedAttnParams& p, int s) {
+  const int* g = p.segs + 4 * (size_t)s;
+  return make_segs(p, g[0], g[1], g[2], g[3]);
 }
 
 }  // namespace
@@ -218,11 +220,13 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 // on the line; a share of the allotment stands for the same share of the keys.
 //
 // A share is a list of pieces (a query tile and a run of its key tiles).  Roles:
-//   warp 8      walks the share, describes pieces and key tiles in two small
-//               queues, and loads Q, K and V through TMA; each lane fetches its
-//               page's table entry and issues that page's boxes.  Pages without
-//               a key of the tile are requested past the last page, which TMA
-//               fills with zeros without reading.
+//   warps 8, 10 walk the share and load K (with Q) and V through TMA; each lane
+//               fetches its page's table entry and issues that page's boxes (one
+//               warp alone could not issue the boxes of 16-slot pages in time:
+//               32 tokens over small pages 81 us, with two 63).  Pages without a
+//               key of the tile are requested past the last page, which TMA fills
+//               with zeros without reading.  Warp 8 also describes pieces and key
+//               tiles in two small queues.
 //   warp 9      issues S = Q K^T and O += P V on tcgen05.
 //   warps 0-3 and 4-7   softmax of two streams with their own S, P and O in
 //               TMEM, so that the products of one run during the softmax of the
@@ -230,9 +234,16 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //               A operand of the second product.  O is rescaled only when the
 //               row's maximum grew by more than 2^8 (the kept maximum is then
 //               stale, which the final division cancels).
-// The streams are the even and odd key tiles of one 128-row query tile, merged
-// at the end of a piece, or (PAIR) the two halves of a 256-row query tile, which
-// then share every K and V tile.
+// Query tiles and streams:
+//   kSplit  128 rows; the streams are the even and odd key tiles, merged at the
+//           end of a piece.
+//   kPair   256 rows; the streams are its two halves, which share every K and V
+//           tile.
+//   kQuad   32 rows, in four copies on the 128 lanes of TMEM; the streams are the
+//           even and odd key tiles, and warp w of a stream takes the w-th quarter
+//           of a tile's keys alone (P is zero elsewhere in its copy), so a tile
+//           costs each thread 32 exponentials instead of 128.  The eight partial
+//           results of a row are merged at the end of a piece.
 //
 // A query tile that one CTA did alone is written out.  The parts of a cut tile
 // go to the workspace in fp32, and a second kernel merges them in the order of
@@ -243,6 +254,7 @@ constexpr int kMaxSeqs = 1024;
 constexpr int kQueue = 4, kTileQueue = 8;
 constexpr float kGrow = 8.f;  // log2 of the growth of a maximum that rescales O
 constexpr int kTileCost = 2;  // fixed cost of a query tile, in key tiles
+constexpr int kSplit = kPagedSplit, kPair = kPagedPair, kQuad = kPagedQuad;
 
 struct Piece {
   int r0, nrows, kvh, n;        // first row, rows, kv head, key tiles (-1: no more pieces)
@@ -250,20 +262,23 @@ struct Piece {
   int slot;                     // partial slot: 2 * CTA, + 1 where it is not the CTA's first piece
 };
 
-template <int D, bool PAIR>
+template <int D, int MODE>
 struct PagedCfg {
-  static constexpr int kST = PAIR ? 4 : 5;  // K/V ring tiles
+  // K/V ring tiles: 160 or 128 KB of head_dim 128, and less than twice the key
+  // tile queue (see load_k)
+  static constexpr int kST = D == 128 ? (MODE == kSplit ? 5 : 4) : D == 64 ? 8 : 12;
   static constexpr int kBoxD = D >= 64 ? 64 : D;
   static constexpr int kRowBytes = kBoxD * 2;
   static constexpr int kSw = kRowBytes == 128 ? 2 : 4;
   static constexpr int kNBox = D / kBoxD;
   static constexpr int kBoxBytes = 128 * kRowBytes;
   static constexpr int kTile = 128 * D * 2;  // bytes of a Q, K or V tile
-  static constexpr int kQ = PAIR ? 2 : 1;    // query tiles of 128 rows
+  static constexpr int kQ = MODE == kPair ? 2 : 1;  // query tiles of 128 rows
+  static constexpr int kMerge = MODE == kQuad ? 2 * 128 * (D < 64 ? 16 : 32) * 4 : 0;
   // prefix sums of the units, row and group starts, group of each sequence
   static constexpr int kPlan = 3 * (kMaxSeqs + 4) * 4 + kMaxSeqs * 2;
   static constexpr int kX = 4096;  // (max, sum) of both streams, for two pieces
-  static constexpr size_t kSmem = 1024 + (kQ + kST) * kTile + kPlan + kX +
+  static constexpr size_t kSmem = 1024 + (kQ + kST) * kTile + kMerge + kPlan + kX +
                                   kQueue * sizeof(Piece) + kTileQueue * 16 + 512;
 };
 
@@ -298,6 +313,16 @@ struct Shares {
                    : rem + (int)((unsigned)(u - big) / (unsigned)each);
   }
 };
+
+// Place of a piece's j-th K and V tile in the ring.
+template <bool PAIR>
+DLLM_DEV int k_place(int j) {
+  return PAIR ? 2 * j : j < 2 ? j : 2 * j - 1;
+}
+template <bool PAIR>
+DLLM_DEV int v_place(int j, int n) {
+  return PAIR ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1);
+}
 
 // A wait that ends when another role gave up; sets the flag when it gives up itself.
 DLLM_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
@@ -334,20 +359,22 @@ DLLM_DEV int block_before(int v, int* scratch, int warp, int lane) {
   return before;
 }
 
-template <int D, bool F16, bool PAIR>
+template <int D, bool F16, int MODE>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ PagedAttnParams p) {
-  using C = PagedCfg<D, PAIR>;
+  using C = PagedCfg<D, MODE>;
+  constexpr bool PAIR = MODE == kPair, QUAD = MODE == kQuad;
   constexpr int ST = C::kST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
   uint8_t* q_s = base_s;
   uint8_t* kv_s = q_s + C::kQ * C::kTile;  // [ST]
-  int* upfx = reinterpret_cast<int*>(kv_s + ST * C::kTile);  // [n_seqs + 1]
+  float4* merge_s = reinterpret_cast<float4*>(kv_s + ST * C::kTile);  // [2][4][SW / 4][32]
+  int* upfx = reinterpret_cast<int*>(kv_s + ST * C::kTile + C::kMerge);  // [n_seqs + 1]
   int* rs = upfx + kMaxSeqs + 4;                             // [n_seqs + 1]
   int* gs = rs + kMaxSeqs + 4;                               // [n_groups + 1]
   short* gid = reinterpret_cast<short*>(gs + kMaxSeqs + 4);  // [n_seqs]
@@ -403,14 +430,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr int kPer = (kMaxSeqs + kAttnThreads - 1) / kAttnThreads;
   const int per = (n_seqs + kAttnThreads - 1) / kAttnThreads;
   {
-    int kt[kPer];
+    int kt[kPer], raw[kPer][4];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = t * per + j;
-      kt[j] = j < per && i < n_seqs ? seg_tiles(seq_segs(p, i)) : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        raw[j][k] = j < per && i < n_seqs ? p.segs[4 * (size_t)i + k] : 0;
     }
     for (int i = t; i <= n_seqs; i += kAttnThreads)
       rs[i] = min(max(p.bt.row_start[i], 0), p.bt.n_rows);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      kt[j] = seg_tiles(make_segs(p, raw[j][0], raw[j][1], raw[j][2], raw[j][3]));
     if (p.n_groups > 0) {
       for (int i = t; i <= p.n_groups; i += kAttnThreads) gs[i] = min(max(p.gseq[i], 0), n_seqs);
       for (int i = t; i < n_seqs; i += kAttnThreads) gid[i] = -1;
@@ -490,8 +522,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8) {
-    // ================================================================ producer
+  if (warp == 8 || warp == 10) {
+    // ================================================================ producers
+    const bool k_side = warp == 8;
     const int U = upfx[n_seqs];
     const int G = min((int)gridDim.x, U);  // CTAs with work
     const int cta = blockIdx.x;
@@ -512,7 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       else
         hi = mid;
     }
-    int pos = 0, n_piece = 0, n_q = 0, n_tile = 0;  // ring position; pieces, with keys; key tiles
+    int base = 0, n_piece = 0, n_q = 0, n_tile = 0;  // ring position; pieces, with keys; key tiles
     bool ok = true, first_piece = true;
     const int page_boxes = max(1, kKeyTile >> p.kv.page_shift);
     const int slot_mask = (1 << p.kv.page_shift) - 1;
@@ -593,7 +626,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
       // ---- its description
       const int qi = n_piece % kQueue;
-      if (lane == 0) {
+      if (k_side && lane == 0) {
         ok = n_piece < kQueue ||
              wait_or_abort(&d_empty[qi], (n_piece / kQueue - 1) & 1, p.status, abort);
         if (ok) {
@@ -613,17 +646,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!ok || n == 0) continue;
 
       // ---- its loads
-      if (lane == 0) {
+      if (k_side && lane == 0) {
         ok = n_q == 0 || wait_or_abort(q_empty, (n_q - 1) & 1, p.status, abort);
         if (ok) {
+          constexpr int kCopies = QUAD ? 4 : C::kQ;
           mbar_arrive_expect_tx(q_full,
-                                C::kQ * C::kNBox * p.G * p.rows_per_tile * C::kRowBytes);
+                                kCopies * C::kNBox * p.G * p.rows_per_tile * C::kRowBytes);
 #pragma unroll
-          for (int h = 0; h < C::kQ; ++h)
+          for (int h = 0; h < kCopies; ++h)
 #pragma unroll
             for (int b = 0; b < C::kNBox; ++b)
-              tma_load_3d(q_s + h * C::kTile + b * C::kBoxBytes, &qmap, q_full, b * C::kBoxD,
-                          kvh * p.G, r0 + h * p.rows_per_tile);
+              tma_load_3d(q_s + h * (QUAD ? 32 * C::kRowBytes : C::kTile) + b * C::kBoxBytes,
+                          &qmap, q_full, b * C::kBoxD, kvh * p.G,
+                          r0 + (QUAD ? 0 : h * p.rows_per_tile));
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -668,60 +703,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         return c;
       };
-      auto load = [&](const CUtensorMap* m, const Loc& c) {
-        if (!ok) return;
+      // The tiles are in the ring in the order the products take them: K0 K1 V0 K2
+      // V1 ... or (pairs) K0 V0 K1 V1 ...  The description of a key tile goes with
+      // its K.  Its slot is free: the ring is shorter than two tiles for each slot
+      // of the queue, so the softmax is done with the tile that had the slot.
+      Loc c = locate(k0);
+      for (int j = 0; ok && j < n; ++j) {
+        Loc next = c;
+        if (j + 1 < n) next = locate(k0 + j + 1);
+        const int pos = base + (k_side ? k_place<PAIR>(j) : v_place<PAIR>(j, n));
         const int st = pos % ST;
         if (lane == 0) {
           ok = pos < ST || wait_or_abort(&kv_empty[st], (pos / ST - 1) & 1, p.status, abort);
           if (ok) mbar_arrive_expect_tx(&kv_full[st], C::kTile);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) return;
+        if (!ok) break;
         if (lane < page_boxes) {
           uint8_t* dst = kv_s + st * C::kTile + lane * page_keys * C::kRowBytes;
 #pragma unroll
           for (int b = 0; b < C::kNBox; ++b)
-            tma_load_4d(dst + b * C::kBoxBytes, m, &kv_full[st], b * C::kBoxD,
-                        page_keys == kKeyTile ? c.kb & slot_mask : 0, kvh, c.page);
+            tma_load_4d(dst + b * C::kBoxBytes, k_side ? &kmap : &vmap, &kv_full[st],
+                        b * C::kBoxD, page_keys == kKeyTile ? c.kb & slot_mask : 0, kvh, c.page);
         }
-        ++pos;
-      };
-      // The description of a key tile goes with its K.  Its slot is free: the K
-      // ring is shorter than the queue, so the softmax is done with the tile
-      // that had the slot.
-      auto load_k = [&](const Loc& c) {
-        load(&kmap, c);
-        if (ok && lane == 0) {
-          tiles_s[n_tile % kTileQueue] = make_int4(c.kb, c.kl, c.kh, c.w);
-          mbar_arrive(&t_full[n_tile % kTileQueue]);
+        if (k_side && lane == 0) {
+          const int ti = (n_tile + j) % kTileQueue;
+          tiles_s[ti] = make_int4(c.kb, c.kl, c.kh, c.w);
+          mbar_arrive(&t_full[ti]);
         }
-        ++n_tile;
-      };
-      if constexpr (PAIR) {  // in the order the products take them: K0 V0 K1 V1 ...
-        Loc a = locate(k0);
-        for (int j = 0; ok && j < n; ++j) {
-          Loc b = a;
-          load_k(a);
-          if (j + 1 < n) b = locate(k0 + j + 1);
-          load(&vmap, a);
-          a = b;
-        }
-      } else {  // K0 K1 V0 K2 V1 ...
-        Loc a = locate(k0), b = a;
-        if (n > 1) b = locate(k0 + 1);
-        load_k(a);
-        if (n > 1) load_k(b);
-        for (int j = 0; ok && j < n; ++j) {
-          Loc c = b;
-          if (j + 2 < n) c = locate(k0 + j + 2);
-          load(&vmap, a);
-          if (j + 2 < n) load_k(c);
-          a = b;
-          b = c;
-        }
+        c = next;
       }
+      n_tile += n;
+      base += 2 * n;
     }
-    if (lane == 0) {
+    if (k_side && lane == 0) {
       const int qi = n_piece % kQueue;
       if (ok && (n_piece < kQueue ||
                  wait_or_abort(&d_empty[qi], (n_piece / kQueue - 1) & 1, p.status, abort))) {
@@ -729,11 +744,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_arrive(&d_full[qi]);
       }
       p.cut[cta] = cut;
-      if (*abort) {  // copies in flight land before the block goes
-        for (int x = max(0, pos - ST); x < pos; ++x)
-          mbar_wait(&kv_full[x % ST], (x / ST) & 1, p.status);
-        if (n_q > 0) mbar_wait(q_full, (n_q - 1) & 1, p.status);
-      }
+    }
+    if (*abort) {  // copies in flight land before the block goes
+      const unsigned long long t0 = global_ns();
+      while (global_ns() - t0 < 100000ull) __nanosleep(1000);
     }
   } else if (warp == 9) {
     // ================================================================ products
@@ -754,14 +768,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ++n_piece;
         if (n < 0) break;
         if (n == 0) continue;
-        auto k_pos = [&](int j) { return base + (PAIR ? 2 * j : j < 2 ? j : 2 * j - 1); };
-        auto v_pos = [&](int j) { return base + (PAIR ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1)); };
         auto wait_kv = [&](int ps) {
           return wait_or_abort(&kv_full[ps % ST], (ps / ST) & 1, p.status, abort);
         };
         // S of key tile j in stream x; the tile and Q are free after its last use
         auto s_mma = [&](int x, int j, bool k_last) {
-          const int ps = k_pos(j);
+          const int ps = base + k_place<PAIR>(j);
           if (!wait_kv(ps)) return false;
           tc_fence_after();
           const uint32_t ka = kva + (ps % ST) * C::kTile;
@@ -779,7 +791,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           return true;
         };
         auto pv_mma = [&](int x, int j, bool accumulate, bool v_last) {
-          const int ps = v_pos(j);
+          const int ps = base + v_place<PAIR>(j, n);
           if (!wait_or_abort(&p_full[x], cnt[x] & 1, p.status, abort) || !wait_kv(ps))
             return false;
           ++cnt[x];
@@ -819,7 +831,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_off + wg * 128;
     const uint32_t o_tm = tmem + lane_off + 256;
-    const int row_in = row / p.G, hh = row - row_in * p.G;
+    const int qrow = QUAD ? lane : row;  // row of the query tile (of its half)
+    const int row_in = qrow / p.G, hh = qrow - row_in * p.G;
     const int rr = row_in + (PAIR ? wg * p.rows_per_tile : 0);  // row within the query tile
     const int page_keys = min(kKeyTile, 1 << p.kv.page_shift);
     int n_piece = 0, n_q = 0, s_cnt = 0, kv_base = 0, n_tile = 0;
@@ -838,6 +851,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int r = d.r0 + rr;
       const int limit = valid && p.row_limit != nullptr ? p.row_limit[r] : INT_MAX;
       float m = -FLT_MAX, l = 0.f;
+      // take the new maximum over; O and the sum are rescaled when it grew a lot
+      auto grow = [&](bool first, float m_new) {
+        if (first) {
+          m = m_new;
+        } else if (__any_sync(0xffffffffu, valid && m_new > m + kGrow)) {
+          // S of this tile is complete, hence also the products before it
+          const float alpha = fast_exp2(m - m_new);
+          m = m_new;
+          l *= alpha;
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            float v[16];
+            tmem_ld16(o_tm + wg * 128 + c * 16, v);
+            tmem_ld_wait16(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] *= alpha;
+            tmem_st16(o_tm + wg * 128 + c * 16, v);
+          }
+        }
+      };
       const int j0 = PAIR ? 0 : wg;
       for (int j = j0; stream && j < d.n; j += PAIR ? 1 : 2) {
         const int ti = n_tile + j;
@@ -852,7 +885,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool member = valid && rr >= (tl.w & 511) && rr < ((tl.w >> 9) & 511);
         const int first_k = tl.y - tl.x;
         const int end_k = member ? min(tl.z, own ? limit : INT_MAX) - tl.x : 0;
-        if (__any_sync(0xffffffffu, end_k > first_k)) {
+        if (!__any_sync(0xffffffffu, end_k > first_k)) {
+          if (active) {  // no row of this warp sees the tile
+            const float none[16] = {};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_st16(s_tm + c * 16, none);
+            tmem_st_wait();
+          }
+        } else if constexpr (QUAD) {
+          const int q0 = (warp & 3) * 32;  // this warp's quarter of the keys
+          float s[32];
+          tmem_ld32(s_tm + q0, s);
+          tmem_ld_wait32(s);
+          if (__any_sync(0xffffffffu, valid && (first_k > q0 || end_k < q0 + 32))) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (q0 + i < first_k || q0 + i >= end_k) s[i] = -INFINITY;
+          }
+          float mx[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+          const float m_new =
+              fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
+          grow(j == j0, m_new);
+          float pk[16], ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float p0 = fast_exp2(fmaf(s[2 * i], p.scale_log2, -m));
+            const float p1 = fast_exp2(fmaf(s[2 * i + 1], p.scale_log2, -m));
+            ls[i & 3] += p0 + p1;
+            pk[i] = __uint_as_float(pack2<F16>(p0, p1));
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          const float none[16] = {};
+#pragma unroll
+          for (int c = 1; c < 4; ++c) tmem_st16(s_tm + (((warp & 3) + c) & 3) * 16, none);
+          tmem_st16(s_tm + (warp & 3) * 16, pk);
+          tmem_st_wait();
+        } else {
           // TMEM is read twice, for the maximum and for the probabilities, 32
           // columns at a time: few registers and little code
           if (__any_sync(0xffffffffu, valid && (first_k > 0 || end_k < kKeyTile))) {
@@ -882,23 +952,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           const float m_new =
               fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
-          if (j == j0) {
-            m = m_new;
-          } else if (__any_sync(0xffffffffu, valid && m_new > m + kGrow)) {
-            // S of this tile is complete, hence also the products before it
-            const float alpha = fast_exp2(m - m_new);
-            m = m_new;
-            l *= alpha;
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              float v[16];
-              tmem_ld16(o_tm + wg * 128 + c * 16, v);
-              tmem_ld_wait16(v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] *= alpha;
-              tmem_st16(o_tm + wg * 128 + c * 16, v);
-            }
-          }
+          grow(j == j0, m_new);
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
           float s0[32], s1[32];
           auto probs = [&](const float (&x)[32], int c) {
@@ -925,19 +979,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
           tmem_st_wait();
-        } else if (active) {  // no row of this warp sees the tile
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) pk[i] = 0u;
-          tmem_st32(s_tm, pk);
-          tmem_st32(s_tm + 32, pk);
-          tmem_st_wait();
         }
         // Slots of a loaded page outside the tile's range may hold anything,
         // infinities and NaN included: their weight is zero, their values have
         // to be as well.
         if (tl.y > tl.x || tl.z < tl.x + kKeyTile) {
-          const int vp = kv_base + (PAIR ? 2 * j + 1 : min(2 * j + 2, 2 * d.n - 1));
+          const int vp = kv_base + v_place<PAIR>(j, d.n);
           const int key = tl.x + row;
           const int pg = key & ~(page_keys - 1);
           ok = wait_or_abort(&kv_full[vp % ST], (vp / ST) & 1, p.status, abort);
@@ -965,11 +1012,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           float2* x = reinterpret_cast<float2*>(x_s) + (n_q & 1) * 256;
           x[wg * 128 + row] = make_float2(m, l);
           named_bar_sync(1, 256);
-          const float2 y0 = x[row], y1 = x[128 + row];
+          const float2 y0 = x[row], y1 = x[128 + row];  // a stream without tiles has sum 0
           mt = fmaxf(y0.x, y1.x);
+          if constexpr (QUAD) {
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+              mt = fmaxf(mt, fmaxf(x[(row + 32 * k) & 127].x, x[128 + ((row + 32 * k) & 127)].x));
+            lt = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {  // the same order in every warp
+              const float2 y = x[k * 32 + lane];
+              lt += y.y * fast_exp2(y.x - mt);
+            }
+          }
           a0 = fast_exp2(y0.x - mt);
-          a1 = d.n > 1 ? fast_exp2(y1.x - mt) : 0.f;
-          lt = y0.y * a0 + (d.n > 1 ? y1.y * a1 : 0.f);
+          a1 = fast_exp2(y1.x - mt);
+          if constexpr (!QUAD) lt = y0.y * a0 + y1.y * a1;
         }
         ok = wait_or_abort(o_full, n_q & 1, p.status, abort);
         if (!ok) break;
@@ -980,15 +1038,93 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       constexpr int kC = kCols < 32 ? kCols : 32;
       const int c0 = PAIR ? 0 : wg * kCols;
       const int head = d.kvh * p.G + hh;
-      const size_t part_row = (size_t)d.slot * p.slot_rows + (PAIR ? wg * 128 : 0) + row;
-      if (active) {
-        if (d.parts == 1) {
-          const float inv = lt > 0.f ? 1.f / lt : 0.f;
-          a0 *= inv;
-          a1 *= inv;
+      const size_t part_row = (size_t)d.slot * p.slot_rows + (PAIR ? wg * 128 : 0) + qrow;
+      if (d.parts == 1) {
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        a0 *= inv;
+        a1 *= inv;
+      }
+      uint16_t* out = static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride +
+                      head * p.out.head_stride + c0;
+      if constexpr (QUAD) {
+        // each warp brings the sum of its streams for its quarter of the keys; the
+        // four are added through shared memory, SW columns at a time, of which
+        // each warp finishes SW / 4
+        constexpr int SW = kC, kOwn = SW / 4;
+        float v[kCols / SW][SW];
+#pragma unroll
+        for (int c = 0; c < kCols / SW; ++c) {
+#pragma unroll
+          for (int i = 0; i < SW; ++i) v[c][i] = 0.f;
+          if (d.n > 0 && active) {
+            float w[SW];
+            const uint32_t at = o_tm + c0 + c * SW;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (x >= d.n) break;
+              if constexpr (SW == 32) {
+                tmem_ld32(at + x * 128, w);
+                tmem_ld_wait32(w);
+              } else {
+                tmem_ld16(at + x * 128, reinterpret_cast<float(&)[16]>(w));
+                tmem_ld_wait16(w);
+              }
+#pragma unroll
+              for (int i = 0; i < SW; ++i) v[c][i] = fmaf(w[i], x ? a1 : a0, v[c][i]);
+            }
+          }
         }
-        uint16_t* out = static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride +
-                        head * p.out.head_stride + c0;
+        if (d.n > 0) {
+          tc_fence_before();
+          mbar_arrive(o_empty);
+        }
+        float4* ms = merge_s + wg * (4 * SW / 4 * 32);
+#pragma unroll
+        for (int c = 0; c < kCols / SW; ++c) {
+          named_bar_sync(2 + wg, 128);  // the buffer is free
+#pragma unroll
+          for (int k = 0; k < SW / 4; ++k)
+            ms[((warp & 3) * (SW / 4) + k) * 32 + lane] =
+                make_float4(v[c][4 * k], v[c][4 * k + 1], v[c][4 * k + 2], v[c][4 * k + 3]);
+          named_bar_sync(2 + wg, 128);
+          float o[kOwn];
+#pragma unroll
+          for (int k = 0; k < kOwn / 4; ++k) {
+            const int at = ((warp & 3) * (kOwn / 4) + k) * 32 + lane;
+            float4 z = ms[at];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+              const float4 y = ms[at + w * (SW / 4) * 32];
+              z.x += y.x;
+              z.y += y.y;
+              z.z += y.z;
+              z.w += y.w;
+            }
+            o[4 * k] = z.x;
+            o[4 * k + 1] = z.y;
+            o[4 * k + 2] = z.z;
+            o[4 * k + 3] = z.w;
+          }
+          if (valid) {
+            const int col = c * SW + (warp & 3) * kOwn;
+            if (d.parts == 1) {
+              uint32_t u[kOwn / 2];
+#pragma unroll
+              for (int i = 0; i < kOwn / 2; ++i) u[i] = pack2<F16>(o[2 * i], o[2 * i + 1]);
+              if constexpr (kOwn == 8)
+                *reinterpret_cast<uint4*>(out + col) = make_uint4(u[0], u[1], u[2], u[3]);
+              else
+                *reinterpret_cast<uint2*>(out + col) = make_uint2(u[0], u[1]);
+            } else if (lt > 0.f) {
+              float* part = p.part + part_row * D + c0 + col;
+#pragma unroll
+              for (int i = 0; i < kOwn; i += 4)
+                *reinterpret_cast<float4*>(part + i) =
+                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+          }
+        }
+      } else if (active) {
         float* part = p.part + part_row * D + c0;
 #pragma unroll 1
         for (int c = 0; c < kCols / kC; ++c) {
@@ -1034,11 +1170,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
       }
-      if (d.n > 0) {
+      if (!QUAD && d.n > 0) {
         tc_fence_before();
         mbar_arrive(o_empty);
       }
-      if (valid && (PAIR || wg == 0)) {
+      if (valid && (PAIR || warp == 0 || (!QUAD && wg == 0))) {
         if (d.parts > 1)
           p.part_ml[part_row] = make_float2(mt, lt);
         else if (p.lse != nullptr)
@@ -1166,28 +1302,39 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 
 namespace {
 
+template <int D, bool F16, int MODE>
+cudaError_t launch_mode(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+                        const PagedAttnParams& p, cudaStream_t s) {
+  return launch_pdl(paged_attn_kernel<D, F16, MODE>, dim3(kNumSMs), dim3(kAttnThreads),
+                    PagedCfg<D, MODE>::kSmem, s, qm, km, vm, p);
+}
+
 template <int D, bool F16>
 cudaError_t launch_paged_attn_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
-                                const PagedAttnParams& p, bool pair, cudaStream_t s) {
-  const dim3 grid(kNumSMs), block(kAttnThreads);
-  const cudaError_t e = pair ? launch_pdl(paged_attn_kernel<D, F16, true>, grid, block,
-                                          PagedCfg<D, true>::kSmem, s, qm, km, vm, p)
-                             : launch_pdl(paged_attn_kernel<D, F16, false>, grid, block,
-                                          PagedCfg<D, false>::kSmem, s, qm, km, vm, p);
+                                const PagedAttnParams& p, int mode, cudaStream_t s) {
+  const cudaError_t e = mode == kPair   ? launch_mode<D, F16, kPair>(qm, km, vm, p, s)
+                        : mode == kQuad ? launch_mode<D, F16, kQuad>(qm, km, vm, p, s)
+                                        : launch_mode<D, F16, kSplit>(qm, km, vm, p, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged_merge_kernel<D, F16>, dim3(kNumSMs, kMergeY), dim3(kMergeWarps * 32), 0,
                     s, p);
 }
 
+template <int D, bool F16, int MODE>
+cudaError_t prepare_mode() {
+  static_assert(PagedCfg<D, MODE>::kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(PagedCfg<D, MODE>::kST <= 13, "ring places, see the key tile queue");
+  return cudaFuncSetAttribute(paged_attn_kernel<D, F16, MODE>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)PagedCfg<D, MODE>::kSmem);
+}
+
 template <int D, bool F16>
 cudaError_t prepare_t() {
-  const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, F16, false>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)PagedCfg<D, false>::kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(paged_attn_kernel<D, F16, true>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)PagedCfg<D, true>::kSmem);
+  cudaError_t e = prepare_mode<D, F16, kSplit>();
+  if (e == cudaSuccess) e = prepare_mode<D, F16, kPair>();
+  if (e == cudaSuccess) e = prepare_mode<D, F16, kQuad>();
+  return e;
 }
 
 }  // namespace
@@ -1203,15 +1350,15 @@ cudaError_t paged_attn_prepare() {
 }
 
 cudaError_t launch_paged_attn(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
-                              const PagedAttnParams& p, bool pair, cudaStream_t s) {
+                              const PagedAttnParams& p, int mode, cudaStream_t s) {
   const int D = p.kv.D;
   if (p.kv.f16)
-    return D == 128  ? launch_paged_attn_t<128, true>(qm, km, vm, p, pair, s)
-           : D == 64 ? launch_paged_attn_t<64, true>(qm, km, vm, p, pair, s)
-                     : launch_paged_attn_t<32, true>(qm, km, vm, p, pair, s);
-  return D == 128  ? launch_paged_attn_t<128, false>(qm, km, vm, p, pair, s)
-         : D == 64 ? launch_paged_attn_t<64, false>(qm, km, vm, p, pair, s)
-                   : launch_paged_attn_t<32, false>(qm, km, vm, p, pair, s);
+    return D == 128  ? launch_paged_attn_t<128, true>(qm, km, vm, p, mode, s)
+           : D == 64 ? launch_paged_attn_t<64, true>(qm, km, vm, p, mode, s)
+                     : launch_paged_attn_t<32, true>(qm, km, vm, p, mode, s);
+  return D == 128  ? launch_paged_attn_t<128, false>(qm, km, vm, p, mode, s)
+         : D == 64 ? launch_paged_attn_t<64, false>(qm, km, vm, p, mode, s)
+                   : launch_paged_attn_t<32, false>(qm, km, vm, p, mode, s);
 }
 
 }  // namespace dllm

@@ -86,10 +86,14 @@ dllm_status check_heads(int n_q_heads, const PagedPool& kv) {
   return DLLM_OK;
 }
 
-// Query tiles of 256 rows share every key tile between two halves; they are
-// taken when an item (a group, or a sequence without one) has more than 128
-// query rows on average.
-bool pair_tiles(long long n_rows, int items, int G) { return n_rows * G > 128ll * items; }
+// Query tiles by the average query rows of an item (a group, or a sequence
+// without one): up to 32 rows the 32-row tiles, whose softmax is spread over all
+// warps; above 128 the 256-row ones, whose halves share every key tile.
+int query_tiles(long long n_rows, int items, int G) {
+  const long long rows = n_rows * G;
+  return G <= 32 && rows <= 32ll * items ? kPagedQuad : rows > 128ll * items ? kPagedPair
+                                                                             : kPagedSplit;
+}
 
 // Workspace: status word, a record per CTA, the parts of cut query tiles.
 constexpr size_t kWsCut = 256, kWsParts = 4096;
@@ -163,21 +167,22 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
     p.plen = groups->len;
   }
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return DLLM_ERR_INVALID;
-  // The line of work units (key tiles, and a cost per query tile) has 32-bit
-  // coordinates: its length at the tables' full width has to fit.
-  const int g128 = 128 / (n_q_heads / p.kv.Hkv);
-  const long long own_tiles = (((long long)p.bt.max_pages << p.kv.page_shift) + 127) / 128;
-  const long long pre_tiles = (((long long)p.pmax_pages << p.kv.page_shift) + 127) / 128;
-  const long long q_tiles = p.bt.n_rows / g128 + p.bt.n_seqs;
-  if (q_tiles * p.kv.Hkv * (2 * own_tiles + pre_tiles + 8) >= (1ll << 31))
-    return DLLM_ERR_UNSUPPORTED;
   p.Hq = n_q_heads;
   p.G = n_q_heads / p.kv.Hkv;
   p.slot_rows = slot_rows(p.bt.n_rows, p.G);
   if (ws_bytes < workspace_bytes(p.kv, p.slot_rows)) return DLLM_ERR_WORKSPACE;
+  const int mode = query_tiles(p.bt.n_rows, groups ? p.n_groups : p.bt.n_seqs, p.G);
+  if (mode == kPagedQuad) p.slot_rows = std::min(p.slot_rows, 32);
   const int D = p.kv.D;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  p.rows_per_tile = 128 / p.G;
+  p.rows_per_tile = (mode == kPagedQuad ? 32 : 128) / p.G;
+  // The line of work units (key tiles, and a cost per query tile) has 32-bit
+  // coordinates: its length at the tables' full width has to fit.
+  const long long own_tiles = (((long long)p.bt.max_pages << p.kv.page_shift) + 127) / 128;
+  const long long pre_tiles = (((long long)p.pmax_pages << p.kv.page_shift) + 127) / 128;
+  const long long q_tiles = p.bt.n_rows / p.rows_per_tile + p.bt.n_seqs;
+  if (q_tiles * p.kv.Hkv * (2 * own_tiles + pre_tiles + 8) >= (1ll << 31))
+    return DLLM_ERR_UNSUPPORTED;
   p.segs = segs;
   p.row_limit = row_limit;
   p.scale_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.f / sqrtf((float)D));
@@ -200,8 +205,7 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
   if (!make_map(&qm, p.q.data, 3, qd, qs, qb, D) || !make_map(&km, p.kv.k, 4, kd, ks, kb, D) ||
       !make_map(&vm, p.kv.v, 4, kd, ks, kb, D))
     return DLLM_ERR_CUDA;
-  const bool pair = pair_tiles(p.bt.n_rows, groups ? p.n_groups : p.bt.n_seqs, p.G);
-  return launch_paged_attn(qm, km, vm, p, pair, reinterpret_cast<cudaStream_t>(stream)) ==
+  return launch_paged_attn(qm, km, vm, p, mode, reinterpret_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? DLLM_OK
              : DLLM_ERR_CUDA;

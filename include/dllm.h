@@ -359,9 +359,8 @@ dllm_status dllm_decode_all(const dllm_config* cfg, const dllm_weights* w, const
  * Supported: head_dim 32, 64 or 128; page_size a power of two in [8, 65536];
  * n_q_heads a multiple of n_kv_heads, at most 128 query heads per kv head;
  * n_seqs and n_groups <= 1024; n_rows < 2^24; max_pages * page_size <= 2^24;
- * for attention, 128-row query tiles times 128-position key tiles times kv heads
- * at the tables' full width (about (n_rows * n_q_heads / 128 + n_seqs *
- * n_kv_heads) * max_pages * page_size / 64) < 2^31.
+ * for attention, work units (query tiles of 32 query rows or more, times kv
+ * heads, times twice the 128-position key tiles of a table row) < 2^31.
  * Data pointers must be 16-byte aligned and all strides multiples of 16 bytes
  * (8 elements); the head_dim elements of a head are contiguous. */
 typedef enum { DLLM_KV_BF16 = 0, DLLM_KV_F16 = 1 } dllm_kv_type;
