@@ -227,7 +227,9 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //               key of the tile are requested past the last page, which TMA fills
 //               with zeros without reading.  Warp 8 also describes pieces and key
 //               tiles in two small queues.
-//   warp 9      issues S = Q K^T and O += P V on tcgen05.
+//   warp 9      issues S = Q K^T and O += P V on tcgen05.  (One warp for each stream
+//               let the streams' products interleave and their softmaxes run at the
+//               same time: 187 us instead of 161 for the 32 samples.)
 //   warps 0-3 and 4-7   softmax of two streams with their own S, P and O in
 //               TMEM, so that the products of one run during the softmax of the
 //               other.  A thread owns a query row; P overwrites S in TMEM as the
@@ -235,12 +237,12 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //               row's maximum grew by more than 2^8 (the kept maximum is then
 //               stale, which the final division cancels).
 // Query tiles and streams:
-//   kSplit  128 rows; the streams are the even and odd key tiles, merged at the
+//   kSplit  128 rows; the streams take key tiles in turn and are merged at the
 //           end of a piece.
 //   kPair   256 rows; the streams are its two halves, which share every K and V
 //           tile.
-//   kQuad   32 rows, in four copies on the 128 lanes of TMEM; the streams are the
-//           even and odd key tiles, and warp w of a stream takes the w-th quarter
+//   kQuad   32 rows, in four copies on the 128 lanes of TMEM; the streams take key
+//           tiles in turn, and warp w of a stream takes the w-th quarter
 //           of a tile's keys alone (P is zero elsewhere in its copy), so a tile
 //           costs each thread 32 exponentials instead of 128.  The eight partial
 //           results of a row are merged at the end of a piece.
@@ -264,9 +266,9 @@ struct Piece {
 
 template <int D, int MODE>
 struct PagedCfg {
-  // K/V ring tiles: 160 or 128 KB of head_dim 128, and less than twice the key
-  // tile queue (see load_k)
-  static constexpr int kST = D == 128 ? (MODE == kSplit ? 5 : 4) : D == 64 ? 8 : 12;
+  // tiles of the K ring (2 to 6, see the key tile queue) and of the V ring
+  static constexpr int kSTK = D == 128 ? (MODE == kSplit ? 3 : 2) : D == 64 ? 4 : 6;
+  static constexpr int kSTV = D == 128 ? 2 : D == 64 ? 4 : 6;
   static constexpr int kBoxD = D >= 64 ? 64 : D;
   static constexpr int kRowBytes = kBoxD * 2;
   static constexpr int kSw = kRowBytes == 128 ? 2 : 4;
@@ -275,10 +277,11 @@ struct PagedCfg {
   static constexpr int kTile = 128 * D * 2;  // bytes of a Q, K or V tile
   static constexpr int kQ = MODE == kPair ? 2 : 1;  // query tiles of 128 rows
   static constexpr int kMerge = MODE == kQuad ? 2 * 128 * (D < 64 ? 16 : 32) * 4 : 0;
-  // prefix sums of the units, row and group starts, group of each sequence
-  static constexpr int kPlan = 3 * (kMaxSeqs + 4) * 4 + kMaxSeqs * 2;
+  // prefix sums of the units, row and group starts, prefix lengths, group of each
+  // sequence
+  static constexpr int kPlan = 4 * (kMaxSeqs + 4) * 4 + kMaxSeqs * 2;
   static constexpr int kX = 4096;  // (max, sum) of both streams, for two pieces
-  static constexpr size_t kSmem = 1024 + (kQ + kST) * kTile + kMerge + kPlan + kX +
+  static constexpr size_t kSmem = 1024 + (kQ + kSTK + kSTV) * kTile + kMerge + kPlan + kX +
                                   kQueue * sizeof(Piece) + kTileQueue * 16 + 512;
 };
 
@@ -314,14 +317,29 @@ struct Shares {
   }
 };
 
-// Place of a piece's j-th K and V tile in the ring.
-template <bool PAIR>
-DLLM_DEV int k_place(int j) {
-  return PAIR ? 2 * j : j < 2 ? j : 2 * j - 1;
-}
-template <bool PAIR>
-DLLM_DEV int v_place(int j, int n) {
-  return PAIR ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1);
+// Transpose of N units of 16 bytes among N neighbouring lanes (N = 2 or 4): after it
+// unit i of a lane is unit (lane % N) of the i-th lane of the group.
+template <int N>
+DLLM_DEV void trade_units(uint4 (&u)[N], int lane) {
+#pragma unroll
+  for (int o = 1; o < N; o <<= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i & o) continue;
+      uint4& a = u[i];
+      uint4& b = u[i | o];
+      uint4 x = up ? a : b;  // what the partner takes
+      x.x = __shfl_xor_sync(0xffffffffu, x.x, o);
+      x.y = __shfl_xor_sync(0xffffffffu, x.y, o);
+      x.z = __shfl_xor_sync(0xffffffffu, x.z, o);
+      x.w = __shfl_xor_sync(0xffffffffu, x.w, o);
+      if (up)
+        a = x;
+      else
+        b = x;
+    }
+  }
 }
 
 // A wait that ends when another role gave up; sets the flag when it gives up itself.
@@ -367,27 +385,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                       const __grid_constant__ PagedAttnParams p) {
   using C = PagedCfg<D, MODE>;
   constexpr bool PAIR = MODE == kPair, QUAD = MODE == kQuad;
-  constexpr int ST = C::kST;
+  constexpr int STK = C::kSTK, STV = C::kSTV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
   uint8_t* q_s = base_s;
-  uint8_t* kv_s = q_s + C::kQ * C::kTile;  // [ST]
-  float4* merge_s = reinterpret_cast<float4*>(kv_s + ST * C::kTile);  // [2][4][SW / 4][32]
-  int* upfx = reinterpret_cast<int*>(kv_s + ST * C::kTile + C::kMerge);  // [n_seqs + 1]
+  uint8_t* k_s = q_s + C::kQ * C::kTile;  // [STK]
+  uint8_t* v_s = k_s + STK * C::kTile;    // [STV]
+  float4* merge_s = reinterpret_cast<float4*>(v_s + STV * C::kTile);  // [2][4][SW / 4][32]
+  int* upfx = reinterpret_cast<int*>(v_s + STV * C::kTile + C::kMerge);  // [n_seqs + 1]
   int* rs = upfx + kMaxSeqs + 4;                             // [n_seqs + 1]
   int* gs = rs + kMaxSeqs + 4;                               // [n_groups + 1]
-  short* gid = reinterpret_cast<short*>(gs + kMaxSeqs + 4);  // [n_seqs]
+  int* pk = gs + kMaxSeqs + 4;                               // [n_groups]
+  short* gid = reinterpret_cast<short*>(pk + kMaxSeqs + 4);  // [n_seqs]
   float* x_s = reinterpret_cast<float*>(gid + kMaxSeqs);
   Piece* queue = reinterpret_cast<Piece*>(x_s + C::kX / 4);
   int4* tiles_s = reinterpret_cast<int4*>(queue + kQueue);
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(tiles_s + kTileQueue);  // [ST]
-  uint64_t* kv_empty = kv_full + ST;         // [ST]
-  uint64_t* d_full = kv_empty + ST;          // [kQueue]
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(tiles_s + kTileQueue);  // [STK]
+  uint64_t* k_empty = k_full + STK;          // [STK]
+  uint64_t* v_full = k_empty + STK;          // [STV]
+  uint64_t* v_empty = v_full + STV;          // [STV]
+  uint64_t* d_full = v_empty + STV;          // [kQueue]
   uint64_t* d_empty = d_full + kQueue;       // [kQueue]
   uint64_t* t_full = d_empty + kQueue;       // [kTileQueue]
   uint64_t* s_full = t_full + kTileQueue;    // [2]
-  uint64_t* p_full = s_full + 2;             // [2]
+  uint64_t* p_half = s_full + 2;             // [2]
+  uint64_t* p_full = p_half + 2;             // [2]
   uint64_t* q_full = p_full + 2;
   uint64_t* q_empty = q_full + 1;
   uint64_t* o_full = q_empty + 1;
@@ -398,9 +421,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int tile_rows = p.rows_per_tile * C::kQ;
   if (t == 0) {
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < STK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < STV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&d_full[i], 1);
@@ -409,6 +436,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int i = 0; i < kTileQueue; ++i) mbar_init(&t_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[i], 128);
       mbar_init(&p_full[i], 128);
     }
     mbar_init(q_full, 1);
@@ -445,6 +473,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       kt[j] = seg_tiles(make_segs(p, raw[j][0], raw[j][1], raw[j][2], raw[j][3]));
     if (p.n_groups > 0) {
       for (int i = t; i <= p.n_groups; i += kAttnThreads) gs[i] = min(max(p.gseq[i], 0), n_seqs);
+      for (int i = t; i < p.n_groups; i += kAttnThreads) pk[i] = prefix_keys(p, i);
       for (int i = t; i < n_seqs; i += kAttnThreads) gid[i] = -1;
     }
     __syncthreads();
@@ -459,10 +488,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncthreads();
     }
     int* scratch = reinterpret_cast<int*>(x_s);
-    int* opfx = reinterpret_cast<int*>(kv_s);  // own key tiles of earlier sequences
+    int* opfx = reinterpret_cast<int*>(k_s);  // own key tiles of earlier sequences
     if (p.n_groups > 0) {
       for (int g = t; g < p.n_groups; g += kAttnThreads)
-        if (prefix_keys(p, g) > 0)
+        if (pk[g] > 0)
           for (int i = gs[g]; i < gs[g + 1]; ++i) gid[i] = (short)g;
       int own[kPer], sum = 0;
 #pragma unroll
@@ -500,7 +529,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int own = opfx[gs[g + 1]] - opfx[i];
           if (nt > 0)
             units[j] = nt * p.kv.Hkv *
-                       (key_tiles(0, prefix_keys(p, g)) + (own + nt - 1) / nt + kTileCost);
+                       (key_tiles(0, pk[g]) + (own + nt - 1) / nt + kTileCost);
         }
       }
       sum += units[j];
@@ -545,7 +574,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       else
         hi = mid;
     }
-    int base = 0, n_piece = 0, n_q = 0, n_tile = 0;  // ring position; pieces, with keys; key tiles
+    int n_piece = 0, n_q = 0, n_tile = 0;  // pieces, with keys; key tiles
+    uint8_t* ring = k_side ? k_s : v_s;
+    uint64_t* full = k_side ? k_full : v_full;
+    uint64_t* empty = k_side ? k_empty : v_empty;
+    const int places = k_side ? STK : STV;
     bool ok = true, first_piece = true;
     const int page_boxes = max(1, kKeyTile >> p.kv.page_shift);
     const int slot_mask = (1 << p.kv.page_shift) - 1;
@@ -615,7 +648,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         sb = s_first;
         load_chunk();
       }
-      const int ktp = g >= 0 ? key_tiles(0, prefix_keys(p, g)) : 0;
+      const int ktp = g >= 0 ? key_tiles(0, pk[g]) : 0;
       const int total = ktp + own_total, allot = cost - kTileCost;
       int k0 = x0 - start - kTileCost, k1 = x1 - start - kTileCost;
       if (total != allot) {
@@ -673,7 +706,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int* table;
         int kk = k;
         if (k < ktp) {
-          x.e0 = prefix_keys(p, g);
+          x.e0 = pk[g];
           table = p.ptable + (size_t)g * p.ptable_stride;
           c.w = nrows << 9;
         } else {
@@ -703,38 +736,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         return c;
       };
-      // The tiles are in the ring in the order the products take them: K0 K1 V0 K2
-      // V1 ... or (pairs) K0 V0 K1 V1 ...  The description of a key tile goes with
-      // its K.  Its slot is free: the ring is shorter than two tiles for each slot
-      // of the queue, so the softmax is done with the tile that had the slot.
+      // The description of a key tile goes with its K.  Its slot in the queue is
+      // free: the K that had this place, at most 6 tiles ago, has been multiplied,
+      // so the softmax is done with the tile two before it.
       Loc c = locate(k0);
       for (int j = 0; ok && j < n; ++j) {
         Loc next = c;
         if (j + 1 < n) next = locate(k0 + j + 1);
-        const int pos = base + (k_side ? k_place<PAIR>(j) : v_place<PAIR>(j, n));
-        const int st = pos % ST;
+        const int ti = n_tile + j, round = (unsigned)ti / (unsigned)places, st = ti - round * places;
         if (lane == 0) {
-          ok = pos < ST || wait_or_abort(&kv_empty[st], (pos / ST - 1) & 1, p.status, abort);
-          if (ok) mbar_arrive_expect_tx(&kv_full[st], C::kTile);
+          ok = round == 0 || wait_or_abort(&empty[st], (round - 1) & 1, p.status, abort);
+          if (ok) mbar_arrive_expect_tx(&full[st], C::kTile);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         if (lane < page_boxes) {
-          uint8_t* dst = kv_s + st * C::kTile + lane * page_keys * C::kRowBytes;
+          uint8_t* dst = ring + st * C::kTile + lane * page_keys * C::kRowBytes;
 #pragma unroll
           for (int b = 0; b < C::kNBox; ++b)
-            tma_load_4d(dst + b * C::kBoxBytes, k_side ? &kmap : &vmap, &kv_full[st],
+            tma_load_4d(dst + b * C::kBoxBytes, k_side ? &kmap : &vmap, &full[st],
                         b * C::kBoxD, page_keys == kKeyTile ? c.kb & slot_mask : 0, kvh, c.page);
         }
         if (k_side && lane == 0) {
-          const int ti = (n_tile + j) % kTileQueue;
-          tiles_s[ti] = make_int4(c.kb, c.kl, c.kh, c.w);
-          mbar_arrive(&t_full[ti]);
+          tiles_s[ti % kTileQueue] = make_int4(c.kb, c.kl, c.kh, c.w);
+          mbar_arrive(&t_full[ti % kTileQueue]);
         }
         c = next;
       }
       n_tile += n;
-      base += 2 * n;
     }
     if (k_side && lane == 0) {
       const int qi = n_piece % kQueue;
@@ -745,83 +774,114 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       p.cut[cta] = cut;
     }
-    if (*abort) {  // copies in flight land before the block goes
-      const unsigned long long t0 = global_ns();
-      while (global_ns() - t0 < 100000ull) __nanosleep(1000);
-    }
   } else if (warp == 9) {
     // ================================================================ products
     if (lane == 0) {
       constexpr uint32_t kIdS = idesc_16(F16, 128, kKeyTile, 0, 0);
       constexpr uint32_t kIdO = idesc_16(F16, 128, D, 0, 1);
-      const uint32_t qa = smem_u32(q_s), kva = smem_u32(kv_s);
-      int base = 0, n_piece = 0, n_q = 0;  // ring position of the piece's first tile
-      int cnt[2] = {0, 0};                 // P tiles taken of each stream
+      const uint64_t q_desc = smem_desc(smem_u32(q_s), 16, 8 * C::kRowBytes, C::kSw);
+      const uint64_t k_desc = smem_desc(smem_u32(k_s), 16, 8 * C::kRowBytes, C::kSw);
+      const uint64_t v_desc = smem_desc(smem_u32(v_s), C::kBoxBytes, 8 * C::kRowBytes, C::kSw);
+      int n_piece = 0, n_q = 0, n_tile = 0;
+      int n_p[2] = {0, 0};  // P tiles taken of each stream
       bool ok = true;
       while (ok) {
         const int qi = n_piece % kQueue;
         ok = wait_or_abort(&d_full[qi], (n_piece / kQueue) & 1, p.status, abort);
         if (!ok) break;
         const int n = queue[qi].n;
-        const bool two = PAIR && queue[qi].nrows > p.rows_per_tile;  // rows in both halves
+        const bool two = queue[qi].nrows > p.rows_per_tile;  // rows in both halves
         mbar_arrive(&d_empty[qi]);
         ++n_piece;
         if (n < 0) break;
         if (n == 0) continue;
-        auto wait_kv = [&](int ps) {
-          return wait_or_abort(&kv_full[ps % ST], (ps / ST) & 1, p.status, abort);
+        auto wait_k = [&](int j) {
+          const int ti = n_tile + j;
+          return wait_or_abort(&k_full[ti % STK], (ti / STK) & 1, p.status, abort);
         };
-        // S of key tile j in stream x; the tile and Q are free after its last use
-        auto s_mma = [&](int x, int j, bool k_last) {
-          const int ps = base + k_place<PAIR>(j);
-          if (!wait_kv(ps)) return false;
-          tc_fence_after();
-          const uint32_t ka = kva + (ps % ST) * C::kTile;
-          const uint32_t qx = qa + (PAIR ? x * C::kTile : 0);
+        auto wait_v = [&](int j) {
+          const int ti = n_tile + j;
+          return wait_or_abort(&v_full[ti % STV], (ti / STV) & 1, p.status, abort);
+        };
+        // S of key tile j in stream x; after the last use K (and Q) are free
+        auto s_mma = [&](int x, int j, bool last) {
+          const int st = (n_tile + j) % STK;
+          const uint64_t kd = k_desc + (uint64_t)(st * C::kTile >> 4);
+          const uint64_t qd = q_desc + (uint64_t)(PAIR ? x * C::kTile >> 4 : 0);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off =
-                (kk * 16 / C::kBoxD) * C::kBoxBytes + ((kk * 16) % C::kBoxD) * 2;
-            umma_bf16(tmem + x * 128, smem_desc(qx + off, 16, 8 * C::kRowBytes, C::kSw),
-                      smem_desc(ka + off, 16, 8 * C::kRowBytes, C::kSw), kIdS, kk > 0);
+            constexpr int kPerBox = C::kBoxD / 16;
+            const int off = (kk / kPerBox) * C::kBoxBytes + (kk % kPerBox) * 32;
+            umma_bf16(tmem + x * 128, qd + (off >> 4), kd + (off >> 4), kIdS, kk > 0);
           }
           umma_commit(&s_full[x]);
-          if (k_last) umma_commit(&kv_empty[ps % ST]);
-          if (k_last && j == n - 1) umma_commit(q_empty);
-          return true;
+          if (last) {
+            umma_commit(&k_empty[st]);
+            if (j == n - 1) umma_commit(q_empty);
+          }
         };
-        auto pv_mma = [&](int x, int j, bool accumulate, bool v_last) {
-          const int ps = base + v_place<PAIR>(j, n);
-          if (!wait_or_abort(&p_full[x], cnt[x] & 1, p.status, abort) || !wait_kv(ps))
-            return false;
-          ++cnt[x];
-          tc_fence_after();
-          const uint32_t va = kva + (ps % ST) * C::kTile;
+        // O of stream x.  128-key rows have the second half of P ready first: where
+        // the whole is not there yet, its products start.
+        auto pv_mma = [&](int x, int j, bool accumulate, bool last) {
+          const int st = (n_tile + j) % STV;
+          const uint64_t vd = v_desc + (uint64_t)(st * C::kTile >> 4);
+          constexpr int kSteps = kKeyTile / 16;
+          // key steps 4 to 7 and then 0 to 3, whatever is there first
+          auto steps = [&](int from, bool acc) {
 #pragma unroll
-          for (int kk = 0; kk < kKeyTile / 16; ++kk)
-            umma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8,
-                        smem_desc(va + kk * 16 * C::kRowBytes, C::kBoxBytes, 8 * C::kRowBytes,
-                                  C::kSw),
-                        kIdO, accumulate || kk > 0);
-          if (v_last) umma_commit(&kv_empty[ps % ST]);
+            for (int k = 0; k < kSteps / 2; ++k)
+              umma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + (from + k) * 8,
+                          vd + ((from + k) * 16 * C::kRowBytes >> 4), kIdO, acc || k > 0);
+          };
+          const uint32_t parity = n_p[x]++ & 1;
+          const bool whole = QUAD || mbar_try_wait(&p_full[x], parity);
+          if (!wait_or_abort(whole ? &p_full[x] : &p_half[x], parity, p.status, abort))
+            return false;
+          tc_fence_after();
+          steps(kSteps / 2, accumulate);
+          if (!whole) {
+            if (!wait_or_abort(&p_full[x], parity, p.status, abort)) return false;
+            tc_fence_after();
+          }
+          steps(0, true);
+          if (last) umma_commit(&v_empty[st]);
           return true;
         };
-        ok = wait_or_abort(q_full, n_q & 1, p.status, abort);
+        ok = wait_or_abort(q_full, n_q & 1, p.status, abort) && wait_k(0);
+        if (!ok) break;
+        tc_fence_after();
         if constexpr (PAIR) {
-          ok = ok && s_mma(0, 0, !two) && (!two || s_mma(1, 0, true));
-          ok = ok && (n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort));
+          s_mma(0, 0, !two);
+          if (two) s_mma(1, 0, true);
+          ok = n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort);
           for (int j = 0; ok && j < n; ++j) {
-            ok = pv_mma(0, j, j > 0, !two) && (j + 1 >= n || s_mma(0, j + 1, !two)) &&
-                 (!two || (pv_mma(1, j, j > 0, true) && (j + 1 >= n || s_mma(1, j + 1, true))));
+            ok = wait_v(j) && pv_mma(0, j, j > 0, !two) && (j + 1 >= n || wait_k(j + 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (j + 1 < n) s_mma(0, j + 1, !two);
+            if (two) {
+              ok = pv_mma(1, j, j > 0, true);
+              if (ok && j + 1 < n) s_mma(1, j + 1, true);
+            }
           }
         } else {
-          ok = ok && s_mma(0, 0, true) && (n < 2 || s_mma(1, 1, true));
+          const int b = n_tile & 1;  // the streams take tiles in turn
+          s_mma(b, 0, true);
+          if (n > 1 && (ok = wait_k(1))) {
+            tc_fence_after();
+            s_mma(b ^ 1, 1, true);
+          }
           ok = ok && (n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort));
-          for (int j = 0; ok && j < n; ++j)
-            ok = pv_mma(j & 1, j, j > 1, true) && (j + 2 >= n || s_mma(j & 1, j + 2, true));
+          for (int j = 0; ok && j < n; ++j) {
+            ok = wait_v(j) && pv_mma((b + j) & 1, j, j > 1, true);
+            if (ok && j + 2 < n && (ok = wait_k(j + 2))) {
+              tc_fence_after();
+              s_mma((b + j) & 1, j + 2, true);
+            }
+          }
         }
         if (ok) umma_commit(o_full);
-        base += 2 * n;
+        n_tile += n;
         ++n_q;
       }
     }
@@ -835,7 +895,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int row_in = qrow / p.G, hh = qrow - row_in * p.G;
     const int rr = row_in + (PAIR ? wg * p.rows_per_tile : 0);  // row within the query tile
     const int page_keys = min(kKeyTile, 1 << p.kv.page_shift);
-    int n_piece = 0, n_q = 0, s_cnt = 0, kv_base = 0, n_tile = 0;
+    int n_piece = 0, n_q = 0, s_cnt = 0, n_tile = 0;
     bool ok = true;
     while (ok) {
       const int qi = n_piece % kQueue;
@@ -871,33 +931,59 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
       };
-      const int j0 = PAIR ? 0 : wg;
+      const int j0 = PAIR ? 0 : (wg ^ n_tile) & 1;  // split: the streams take tiles in turn
       for (int j = j0; stream && j < d.n; j += PAIR ? 1 : 2) {
         const int ti = n_tile + j;
         ok = wait_or_abort(&t_full[ti % kTileQueue], (ti / kTileQueue) & 1, p.status, abort);
         if (!ok) break;
         const int4 tl = tiles_s[ti % kTileQueue];  // base, lo, hi, rows
-        ok = wait_or_abort(&s_full[wg], s_cnt & 1, p.status, abort);
-        if (!ok) break;
-        ++s_cnt;
-        tc_fence_after();
         const bool own = tl.w >> 18;
         const bool member = valid && rr >= (tl.w & 511) && rr < ((tl.w >> 9) & 511);
         const int first_k = tl.y - tl.x;
         const int end_k = member ? min(tl.z, own ? limit : INT_MAX) - tl.x : 0;
-        if (!__any_sync(0xffffffffu, end_k > first_k)) {
+        const bool sees = __any_sync(0xffffffffu, end_k > first_k);
+        const bool masked =
+            __any_sync(0xffffffffu, valid && (first_k > 0 || end_k < kKeyTile));
+        ok = wait_or_abort(&s_full[wg], s_cnt & 1, p.status, abort);
+        if (!ok) break;
+        ++s_cnt;
+        tc_fence_after();
+        // Slots of a loaded page outside the tile's range may hold anything,
+        // infinities and NaN included: their weight is zero, their values have
+        // to be as well.  (S is complete, so the products before it are, and the
+        // V tile that had this place had landed: the wait is for this tile's.)
+        if (tl.y > tl.x || tl.z < tl.x + kKeyTile) {
+          const int key = tl.x + row;
+          const int pg = key & ~(page_keys - 1);
+          ok = wait_or_abort(&v_full[ti % STV], (ti / STV) & 1, p.status, abort);
+          if (!ok) break;
+          if ((key < tl.y || key >= tl.z) && pg < tl.z && pg + page_keys > tl.y) {
+            uint4* v = reinterpret_cast<uint4*>(v_s + (ti % STV) * C::kTile + row * C::kRowBytes);
+#pragma unroll
+            for (int b = 0; b < C::kNBox; ++b)
+#pragma unroll 1
+              for (int c = 0; c < C::kRowBytes / 16; ++c)
+                v[b * (C::kBoxBytes / 16) + c] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (!sees) {
           if (active) {  // no row of this warp sees the tile
             const float none[16] = {};
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_st16(s_tm + c * 16, none);
             tmem_st_wait();
           }
+          if constexpr (!QUAD) {
+            tc_fence_before();
+            mbar_arrive(&p_half[wg]);
+          }
         } else if constexpr (QUAD) {
           const int q0 = (warp & 3) * 32;  // this warp's quarter of the keys
           float s[32];
           tmem_ld32(s_tm + q0, s);
           tmem_ld_wait32(s);
-          if (__any_sync(0xffffffffu, valid && (first_k > q0 || end_k < q0 + 32))) {
+          if (masked) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (q0 + i < first_k || q0 + i >= end_k) s[i] = -INFINITY;
@@ -923,9 +1009,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tmem_st16(s_tm + (warp & 3) * 16, pk);
           tmem_st_wait();
         } else {
-          // TMEM is read twice, for the maximum and for the probabilities, 32
-          // columns at a time: few registers and little code
-          if (__any_sync(0xffffffffu, valid && (first_k > 0 || end_k < kKeyTile))) {
+          // Half of the row stays in registers between the maximum and the
+          // probabilities, the other half is read again.
+          if (masked) {
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               float s[32];
@@ -938,73 +1024,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             tmem_st_wait();
           }
+          constexpr int kH = kKeyTile / 2;
+          float sa[kH], sb[kH];
           float mx[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float s[64];
-            tmem_ld32(s_tm + c * 64, s);
-            tmem_ld32(s_tm + c * 64 + 32, s + 32);
-            tmem_ld_wait32(s);
-            tmem_ld_wait32(s + 32);
+          auto maxima = [&](const float (&x)[kH]) {
 #pragma unroll
-            for (int i = 0; i < 64; i += 2)
-              mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(s[i], s[i + 1]));
-          }
-          const float m_new =
-              fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
-          grow(j == j0, m_new);
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
-          float s0[32], s1[32];
-          auto probs = [&](const float (&x)[32], int c) {
-            float pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float p0 = fast_exp2(fmaf(x[2 * i], p.scale_log2, -m));
-              const float p1 = fast_exp2(fmaf(x[2 * i + 1], p.scale_log2, -m));
-              ls[i & 3] += p0 + p1;
-              pk[i] = __uint_as_float(pack2<F16>(p0, p1));
-            }
-            tmem_st16(s_tm + c * 16, pk);  // below the columns that are still to be read
+            for (int i = 0; i < kH; i += 2)
+              mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(x[i], x[i + 1]));
           };
-          tmem_ld32(s_tm, s0);
-          tmem_ld_wait32(s0);
-#pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            tmem_ld32(s_tm + c * 32 + 32, s1);
-            probs(s0, c);
-            tmem_ld_wait32(s1);
-            if (c == 0) tmem_ld32(s_tm + 64, s0);
-            probs(s1, c + 1);
-            tmem_ld_wait32(s0);
-          }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          auto load_half = [&](int h, float (&x)[kH]) {
+            tmem_ld32(s_tm + h * kH, x);
+            tmem_ld32(s_tm + h * kH + 32, x + 32);
+          };
+          auto landed = [&](float (&x)[kH]) {
+            tmem_ld_wait32(x);
+            tmem_ld_wait32(x + 32);
+          };
+          load_half(0, sa);
+          landed(sa);
+          load_half(1, sb);
+          maxima(sa);
+          landed(sb);
+          maxima(sb);
+          grow(j == j0, fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2));
+          load_half(0, sa);
+          F2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          // P of 64 keys in 32 columns.  (A share of the exponentials as polynomials
+          // on the FMA pipe was slower: the 32 samples' 161 us became 168, 172 and 193
+          // with two, three and four of eight.)
+          auto probs = [&](const float (&x)[kH], uint32_t (&pk)[32]) {
+#pragma unroll
+            for (int i = 0; i < kH; i += 2) {
+              F2 e = fma2(F2{x[i], x[i + 1]}, F2{p.scale_log2, p.scale_log2}, F2{-m, -m});
+              e = F2{fast_exp2(e.x), fast_exp2(e.y)};
+              ls[(i >> 1) & 1] = add2(ls[(i >> 1) & 1], e);
+              pk[i / 2] = pack2<F16>(e.x, e.y);
+            }
+          };
+          uint32_t pk[32];
+          probs(sb, pk);
+          landed(sa);
+          tmem_st32(s_tm + 32, pk);
           tmem_st_wait();
-        }
-        // Slots of a loaded page outside the tile's range may hold anything,
-        // infinities and NaN included: their weight is zero, their values have
-        // to be as well.
-        if (tl.y > tl.x || tl.z < tl.x + kKeyTile) {
-          const int vp = kv_base + v_place<PAIR>(j, d.n);
-          const int key = tl.x + row;
-          const int pg = key & ~(page_keys - 1);
-          ok = wait_or_abort(&kv_full[vp % ST], (vp / ST) & 1, p.status, abort);
-          if (!ok) break;
-          if ((key < tl.y || key >= tl.z) && pg < tl.z && pg + page_keys > tl.y) {
-            uint4* v = reinterpret_cast<uint4*>(kv_s + (vp % ST) * C::kTile + row * C::kRowBytes);
-#pragma unroll
-            for (int b = 0; b < C::kNBox; ++b)
-#pragma unroll
-              for (int c = 0; c < C::kRowBytes / 16; ++c)
-                v[b * (C::kBoxBytes / 16) + c] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
+          tc_fence_before();
+          mbar_arrive(&p_half[wg]);
+          probs(sa, pk);
+          tmem_st32(s_tm, pk);
+          l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+          tmem_st_wait();
         }
         tc_fence_before();
         mbar_arrive(&p_full[wg]);
       }
       if (!ok) break;
+      // split: whether each stream had tiles
+      const bool some0 = d.n > 1 || (d.n == 1 && (n_tile & 1) == 0);
+      const bool some1 = d.n > 1 || (d.n == 1 && (n_tile & 1) == 1);
       n_tile += d.n;
-      kv_base += 2 * d.n;
       // ---- the piece's result
       float a0 = 1.f, a1 = 0.f, mt = m, lt = l;
       if (d.n > 0) {
@@ -1038,7 +1114,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       constexpr int kC = kCols < 32 ? kCols : 32;
       const int c0 = PAIR ? 0 : wg * kCols;
       const int head = d.kvh * p.G + hh;
-      const size_t part_row = (size_t)d.slot * p.slot_rows + (PAIR ? wg * 128 : 0) + qrow;
+      // a slot is [D / 4][slot_rows] groups of four elements: neighbouring rows are
+      // neighbours, as in the lanes that write them
+      const int part_row = (PAIR ? wg * 128 : 0) + qrow;
+      float4* part =
+          reinterpret_cast<float4*>(p.part) + (size_t)d.slot * p.slot_rows * (D / 4) + part_row;
       if (d.parts == 1) {
         const float inv = lt > 0.f ? 1.f / lt : 0.f;
         a0 *= inv;
@@ -1056,12 +1136,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int c = 0; c < kCols / SW; ++c) {
 #pragma unroll
           for (int i = 0; i < SW; ++i) v[c][i] = 0.f;
-          if (d.n > 0 && active) {
+          if (active) {
             float w[SW];
             const uint32_t at = o_tm + c0 + c * SW;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (x >= d.n) break;
+              if (!(x ? some1 : some0)) continue;
               if constexpr (SW == 32) {
                 tmem_ld32(at + x * 128, w);
                 tmem_ld_wait32(w);
@@ -1116,56 +1196,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               else
                 *reinterpret_cast<uint2*>(out + col) = make_uint2(u[0], u[1]);
             } else if (lt > 0.f) {
-              float* part = p.part + part_row * D + c0 + col;
 #pragma unroll
               for (int i = 0; i < kOwn; i += 4)
-                *reinterpret_cast<float4*>(part + i) =
+                part[(c0 + col + i) / 4 * p.slot_rows] =
                     make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
           }
         }
       } else if (active) {
-        float* part = p.part + part_row * D + c0;
 #pragma unroll 1
         for (int c = 0; c < kCols / kC; ++c) {
           float v[kC], w[kC];
-          if (d.n > 0) {
-            const uint32_t at = o_tm + (PAIR ? wg * 128 : 0) + c0 + c * kC;
+          auto add = [&](uint32_t at, float a) {
             if constexpr (kC == 32) {
-              tmem_ld32(at, v);
-              if (!PAIR && d.n > 1) tmem_ld32(at + 128, w);
+              tmem_ld32(at, w);
+              tmem_ld_wait32(w);
             } else {
-              tmem_ld16(at, reinterpret_cast<float(&)[16]>(v));
-              if (!PAIR && d.n > 1) tmem_ld16(at + 128, reinterpret_cast<float(&)[16]>(w));
-            }
-            if constexpr (kC == 32) {
-              tmem_ld_wait32(v);
-              if (!PAIR && d.n > 1) tmem_ld_wait32(w);
-            } else {
-              tmem_ld_wait16(v);
-              if (!PAIR && d.n > 1) tmem_ld_wait16(w);
+              tmem_ld16(at, reinterpret_cast<float(&)[16]>(w));
+              tmem_ld_wait16(w);
             }
 #pragma unroll
-            for (int i = 0; i < kC; ++i) {
-              v[i] *= a0;
-              if (!PAIR && d.n > 1) v[i] = fmaf(w[i], a1, v[i]);
-            }
+            for (int i = 0; i < kC; ++i) v[i] = fmaf(w[i], a, v[i]);
+          };
+#pragma unroll
+          for (int i = 0; i < kC; ++i) v[i] = 0.f;
+          const uint32_t at = o_tm + c0 + c * kC;
+          if constexpr (PAIR) {
+            if (d.n > 0) add(at + wg * 128, a0);
           } else {
-#pragma unroll
-            for (int i = 0; i < kC; ++i) v[i] = 0.f;
+            if (some0) add(at, a0);
+            if (some1) add(at + 128, a1);
           }
-          if (valid) {
-            if (d.parts == 1) {
-#pragma unroll
-              for (int i = 0; i < kC; i += 8)
-                *reinterpret_cast<uint4*>(out + c * kC + i) =
-                    make_uint4(pack2<F16>(v[i], v[i + 1]), pack2<F16>(v[i + 2], v[i + 3]),
-                               pack2<F16>(v[i + 4], v[i + 5]), pack2<F16>(v[i + 6], v[i + 7]));
-            } else if (lt > 0.f) {
+          if (d.parts > 1) {
+            if (valid && lt > 0.f) {
 #pragma unroll
               for (int i = 0; i < kC; i += 4)
-                *reinterpret_cast<float4*>(part + c * kC + i) =
+                part[(c0 + c * kC + i) / 4 * p.slot_rows] =
                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          } else {
+            // 16 bytes a row and store would touch 32 lines: four lanes trade
+            // their units, so that each store covers 16 * kUnits bytes of a row
+            constexpr int kUnits = kC / 8;
+            uint4 un[kUnits];
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i)
+              un[i] = make_uint4(pack2<F16>(v[8 * i], v[8 * i + 1]),
+                                 pack2<F16>(v[8 * i + 2], v[8 * i + 3]),
+                                 pack2<F16>(v[8 * i + 4], v[8 * i + 5]),
+                                 pack2<F16>(v[8 * i + 6], v[8 * i + 7]));
+            trade_units<kUnits>(un, lane);
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+              const int from = (lane & ~(kUnits - 1)) + i;  // the lane whose row this is
+              uint16_t* row_out = reinterpret_cast<uint16_t*>(
+                  __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), from));
+              if (__shfl_sync(0xffffffffu, valid, from))
+                *reinterpret_cast<uint4*>(row_out + c * kC + (lane & (kUnits - 1)) * 8) = un[i];
             }
           }
         }
@@ -1176,12 +1263,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (valid && (PAIR || warp == 0 || (!QUAD && wg == 0))) {
         if (d.parts > 1)
-          p.part_ml[part_row] = make_float2(mt, lt);
+          p.part_ml[(size_t)d.slot * p.slot_rows + part_row] = make_float2(mt, lt);
         else if (p.lse != nullptr)
           p.lse[(size_t)r * p.Hq + head] =
               lt > 0.f ? 0.6931471805599453f * mt + logf(lt) : -INFINITY;
       }
     }
+  }
+  if (*abort) {  // copies and products in flight end before the block goes
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 100000ull) __nanosleep(1000);
   }
   __syncwarp();
   tc_fence_before();
@@ -1193,110 +1284,90 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// Block (c, y) merges rows y, y + kMergeY, ... of the cut query tile that starts
-// in CTA c of the attention kernel: its parts are in that CTA's slot and in the
-// even slots of the CTAs after it.  A warp takes a row, lane i D / 32 of its
-// elements; where the block has fewer rows than warps, several warps share the
-// parts of a row.
-constexpr int kMergeWarps = 8, kMergeY = 16;
+// Block (c, y) merges elements 8y.. 8y + 7 of the rows of the cut query tile that
+// starts in CTA c of the attention kernel: its parts are in that CTA's slot and in
+// the even slots of the CTAs after it.  A lane takes a row, a warp 32 rows; where a
+// tile has fewer rows, several warps share its parts.
+constexpr int kMergeWarps = 8;
 
-template <int D>
 struct RowSum {
-  static constexpr int kE = D / 32;
-  float m = -FLT_MAX, l = 0.f, o[kE];
-  DLLM_DEV RowSum() {
-#pragma unroll
-    for (int i = 0; i < kE; ++i) o[i] = 0.f;
-  }
-  DLLM_DEV void join(float2 ml, const float* v) {
+  float m = -FLT_MAX, l = 0.f, o[8] = {};
+  DLLM_DEV void join(float2 ml, const float4& x, const float4& y) {
     if (ml.y == 0.f) return;  // a part without keys, whose elements are not written
     const float mn = fmaxf(m, ml.x);
     const float a = fast_exp2(m - mn), b = fast_exp2(ml.x - mn);
     m = mn;
     l = l * a + ml.y * b;
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < kE; ++i) o[i] = o[i] * a + v[i] * b;
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * a + v[i] * b;
   }
 };
-template <int N>
-DLLM_DEV void load_n(float* v, const float* src) {
-  if constexpr (N == 4)
-    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-  else if constexpr (N == 2)
-    *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
-  else
-    v[0] = *src;
-}
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
-  constexpr int kE = RowSum<D>::kE;
-  __shared__ float2 ml_s[kMergeWarps];
-  __shared__ float o_s[kMergeWarps][D];
+  __shared__ float2 ml_s[kMergeWarps][32];
+  __shared__ float4 o_s[kMergeWarps][2][32];
   grid_dep_wait();
   grid_dep_launch();
   const int4 cut = p.cut[blockIdx.x];  // first row, rows, kv head, parts | slot parity << 16
   const int parts = cut.w & 0xffff, slot0 = 2 * blockIdx.x + (cut.w >> 16);
-  const int rows = cut.y * p.G;
-  if (parts < 2 || (int)blockIdx.y >= rows) return;
+  if (parts < 2) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int here = (rows - blockIdx.y + kMergeY - 1) / kMergeY;  // rows of this block
-  const int split = here > 4 ? 1 : here > 2 ? 2 : here > 1 ? 4 : 8;
+  // places of the slot in use: 256-row tiles have 128 for each half
+  const int places = cut.y > p.rows_per_tile ? 128 + (cut.y - p.rows_per_tile) * p.G : cut.y * p.G;
+  const int warps = (places + 31) / 32;  // 1 to 8
+  const int split = warps > 4 ? 1 : warps > 2 ? 2 : warps > 1 ? 4 : 8;
   const int wrow = warp / split, wpart = warp - wrow * split;
-  for (int k0 = 0; k0 < here; k0 += kMergeWarps / split) {
-    const int z = (k0 + wrow) * kMergeY + blockIdx.y;
-    const bool have = k0 + wrow < here;
-    const int zr = z / p.G, zh = z - zr * p.G;
-    const int half = zr / p.rows_per_tile;  // 256-row tiles: 128 slots for each half
-    const int at = half * 128 + (zr - half * p.rows_per_tile) * p.G + zh;
-    RowSum<D> sum;
-    if (have) {
-      constexpr int kUn = 4;
-      for (int i = wpart; i < parts; i += kUn * split) {
-        float2 ml[kUn];
-        float v[kUn][kE];
+  const int at = wrow * 32 + lane;
+  const int half = at >> 7, in = at & 127;
+  const int rr = in / p.G + half * p.rows_per_tile, hh = in % p.G;
+  const bool have = at < places && in < p.rows_per_tile * p.G && rr < cut.y;
+  RowSum sum;
+  if (have) {
+    const float4* part = reinterpret_cast<const float4*>(p.part) + 2 * blockIdx.y * p.slot_rows + at;
+    constexpr int kUn = 4;
+    for (int i = wpart; i < parts; i += kUn * split) {
+      float2 ml[kUn];
+      float4 x[kUn], y[kUn];
 #pragma unroll
-        for (int k = 0; k < kUn; ++k) {
-          const int ip = i + k * split;
-          ml[k] = make_float2(-FLT_MAX, 0.f);
-          if (ip < parts) {
-            const size_t ro = (size_t)(ip == 0 ? slot0 : 2 * (blockIdx.x + ip)) * p.slot_rows + at;
-            ml[k] = p.part_ml[ro];
-            load_n<kE>(v[k], p.part + ro * D + lane * kE);
-          }
+      for (int k = 0; k < kUn; ++k) {
+        const int ip = i + k * split;
+        ml[k] = make_float2(-FLT_MAX, 0.f);
+        if (ip < parts) {
+          const size_t ro = (size_t)(ip == 0 ? slot0 : 2 * (blockIdx.x + ip)) * p.slot_rows;
+          ml[k] = p.part_ml[ro + at];
+          x[k] = part[ro * (D / 4)];
+          y[k] = part[ro * (D / 4) + p.slot_rows];
         }
-#pragma unroll
-        for (int k = 0; k < kUn; ++k) sum.join(ml[k], v[k]);
       }
-    }
-    if (split > 1) {
-      if (lane == 0) ml_s[warp] = make_float2(sum.m, sum.l);
 #pragma unroll
-      for (int i = 0; i < kE; ++i) o_s[warp][lane * kE + i] = sum.o[i];
-      __syncthreads();
-      if (wpart == 0)
-        for (int w = warp + 1; w < warp + split; ++w) sum.join(ml_s[w], &o_s[w][lane * kE]);
-      __syncthreads();
+      for (int k = 0; k < kUn; ++k) sum.join(ml[k], x[k], y[k]);
     }
-    if (have && wpart == 0) {
-      const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
-      const int r = cut.x + zr, head = cut.z * p.G + zh;
-      uint16_t* out =
-          static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride + head * p.out.head_stride;
-      if constexpr (kE == 4)
-        *reinterpret_cast<uint2*>(out + 4 * lane) =
-            make_uint2(pack2<F16>(sum.o[0] * inv, sum.o[1] * inv),
-                       pack2<F16>(sum.o[2] * inv, sum.o[3] * inv));
-      else if constexpr (kE == 2)
-        *reinterpret_cast<uint32_t*>(out + 2 * lane) =
-            pack2<F16>(sum.o[0] * inv, sum.o[1] * inv);
-      else
-        out[lane] = (uint16_t)pack2<F16>(sum.o[0] * inv, 0.f);
-      if (lane == 0 && p.lse != nullptr)
-        p.lse[(size_t)r * p.Hq + head] =
-            sum.l > 0.f ? 0.6931471805599453f * sum.m + logf(sum.l) : -INFINITY;
-    }
+  }
+  if (split > 1) {
+    ml_s[warp][lane] = make_float2(sum.m, sum.l);
+    o_s[warp][0][lane] = make_float4(sum.o[0], sum.o[1], sum.o[2], sum.o[3]);
+    o_s[warp][1][lane] = make_float4(sum.o[4], sum.o[5], sum.o[6], sum.o[7]);
+    __syncthreads();
+    if (wpart == 0)
+      for (int w = warp + 1; w < warp + split; ++w)
+        sum.join(ml_s[w][lane], o_s[w][0][lane], o_s[w][1][lane]);
+  }
+  if (have && wpart == 0) {
+    const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
+    const int r = cut.x + rr, head = cut.z * p.G + hh;
+    uint16_t* out =
+        static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride + head * p.out.head_stride;
+    *reinterpret_cast<uint4*>(out + 8 * blockIdx.y) =
+        make_uint4(pack2<F16>(sum.o[0] * inv, sum.o[1] * inv),
+                   pack2<F16>(sum.o[2] * inv, sum.o[3] * inv),
+                   pack2<F16>(sum.o[4] * inv, sum.o[5] * inv),
+                   pack2<F16>(sum.o[6] * inv, sum.o[7] * inv));
+    if (blockIdx.y == 0 && p.lse != nullptr)
+      p.lse[(size_t)r * p.Hq + head] =
+          sum.l > 0.f ? 0.6931471805599453f * sum.m + logf(sum.l) : -INFINITY;
   }
 }
 
@@ -1316,14 +1387,16 @@ cudaError_t launch_paged_attn_t(const CUtensorMap& qm, const CUtensorMap& km, co
                         : mode == kQuad ? launch_mode<D, F16, kQuad>(qm, km, vm, p, s)
                                         : launch_mode<D, F16, kSplit>(qm, km, vm, p, s);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_merge_kernel<D, F16>, dim3(kNumSMs, kMergeY), dim3(kMergeWarps * 32), 0,
-                    s, p);
+  return launch_pdl(paged_merge_kernel<D, F16>, dim3(kNumSMs, D / 8), dim3(kMergeWarps * 32), 0, s,
+                    p);
 }
 
 template <int D, bool F16, int MODE>
 cudaError_t prepare_mode() {
   static_assert(PagedCfg<D, MODE>::kSmem <= 227 * 1024, "shared memory of a CTA");
-  static_assert(PagedCfg<D, MODE>::kST <= 13, "ring places, see the key tile queue");
+  static_assert(PagedCfg<D, MODE>::kSTK >= 2 && PagedCfg<D, MODE>::kSTK <= 6 &&
+                    PagedCfg<D, MODE>::kSTV >= 2,
+                "see the key tile queue");
   return cudaFuncSetAttribute(paged_attn_kernel<D, F16, MODE>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)PagedCfg<D, MODE>::kSmem);
