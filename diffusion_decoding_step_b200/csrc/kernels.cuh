@@ -297,6 +297,7 @@ struct PagedAppendParams {
   const int* pos;
   const int* shift;  // or null
   int rope;          // 0: no rotation
+  int rows_per_block;
   int* status;       // or null
   // turns (2 pi) per position of each pair, theta^(-2i/D) / (2 pi)
   double turns[64];

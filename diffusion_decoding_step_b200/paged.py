@@ -16,15 +16,16 @@ from . import abi
 _TYPES = {torch.bfloat16: abi.DLLM_KV_BF16, torch.float16: abi.DLLM_KV_F16}
 
 
-def _ints(t: torch.Tensor, what: str, shape: tuple, device) -> int:
-    """Address of a contiguous int32 tensor of the given shape (None: any size)."""
-    if t.dtype != torch.int32 or t.device != device or t.dim() != len(shape) \
-            or any(n is not None and n != m for n, m in zip(shape, t.shape)) \
-            or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous int32 tensor of shape "
-                         f"{['any' if n is None else n for n in shape]} on {device} is needed, got "
-                         f"{t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr()
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index; current_stream() costs 2 us
+
+
+def _ints(t: torch.Tensor, what: str, shape: tuple, index: int) -> int:
+    """Address of a contiguous int32 tensor of the given shape on GPU `index`."""
+    if t.dtype is torch.int32 and t.shape == shape and t.get_device() == index \
+            and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what}: a contiguous int32 tensor of shape {list(shape)} on cuda:{index} is "
+                     f"needed, got {t.dtype} {list(t.shape)} on {t.device}")
 
 
 class PagedKV:
@@ -55,52 +56,54 @@ class PagedKV:
             raise ValueError("the D elements of a head have to be contiguous")
         self.k_pages, self.v_pages = k_pages, v_pages
         self.device, self.dtype = k_pages.device, k_pages.dtype
+        self._index = k_pages.get_device()
         n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_pages.shape
         self.n_q_heads, self.max_rows, self.max_groups = n_q_heads, max_rows, max_groups
+        lib = abi.lib()
+        self._append, self._attn = lib.dllm_paged_append, lib.dllm_paged_attn
+        self._shared, self._status = lib.dllm_shared_prefix_attn, lib.dllm_device_status
         self._kv = abi.dllm_kv_pages(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.stride(0),
                                      k_pages.stride(1), k_pages.stride(2), n_pages,
                                      self.page_size, self.n_kv_heads, self.head_dim,
                                      _TYPES[self.dtype])
         self._kv_p = C.byref(self._kv)
         n = C.c_size_t(0)
-        abi.check(abi.dllm_paged_workspace_size(self._kv_p, n_q_heads, max_rows, C.byref(n)), "paged_workspace_size")
+        abi.check(abi.dllm_paged_workspace_size(self._kv_p, n_q_heads, max_rows, C.byref(n)),
+                  "paged_workspace_size")
         self.ws_bytes = int(n.value)
         with torch.cuda.device(self.device):
             self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
             self._ws_p = self.ws.data_ptr()
-            abi.check(abi.dllm_paged_workspace_init(self._ws_p, self.ws_bytes, self._stream()),
+            abi.check(abi.dllm_paged_workspace_init(self._ws_p, self.ws_bytes,
+                                                    _raw_stream(self._index)),
                       "paged_workspace_init")
 
     # ------------------------------------------------------------------ arguments
-    def _stream(self) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream
-
     def _call(self, what: str, fn, *args) -> None:
-        if torch.cuda.current_device() == self.device.index:
-            status = fn(*args, self._stream())
+        if torch.cuda.current_device() == self._index:
+            status = fn(*args, _raw_stream(self._index))
         else:
             with torch.cuda.device(self.device):
-                status = fn(*args, self._stream())
+                status = fn(*args, _raw_stream(self._index))
         if status != abi.DLLM_OK:
             abi.check(status, what)
 
-    def _rows(self, t: torch.Tensor, what: str, n_rows: Optional[int], heads: int):
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim \
-                or t.stride(2) != 1 or t.dtype != self.dtype or t.device != self.device \
-                or (n_rows is not None and t.shape[0] != n_rows):
-            raise ValueError(f"{what}: a {self.dtype} tensor [{n_rows or 'rows'}][{heads}]"
-                             f"[{self.head_dim}] on {self.device} with contiguous heads is needed, "
-                             f"got {t.dtype} {list(t.shape)} on {t.device}")
-        return C.byref(abi.dllm_rows(t.data_ptr(), t.stride(0), t.stride(1)))
+    def _rows(self, t: torch.Tensor, what: str, n_rows: int, heads: int):
+        if t.dtype is self.dtype and t.shape == (n_rows, heads, self.head_dim) \
+                and t.get_device() == self._index:
+            row, head, one = t.stride()
+            if one == 1:
+                return C.byref(abi.dllm_rows(t.data_ptr(), row, head))
+        raise ValueError(f"{what}: a {self.dtype} tensor [{n_rows}][{heads}][{self.head_dim}] on "
+                         f"{self.device} with contiguous heads is needed, got {t.dtype} "
+                         f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
 
     def _batch(self, n_rows: int, row_start: torch.Tensor, page_table: torch.Tensor):
-        n = row_start.shape[0] - 1 if row_start.dim() == 1 else 0
-        if n < 1:
-            raise ValueError("row_start: an int32 tensor [n_seqs + 1] is needed")
-        rs = _ints(row_start, "row_start", (n + 1,), self.device)
-        tab = _ints(page_table, "page_table", (n, None), self.device)
-        width = page_table.shape[1]
-        return n, C.byref(abi.dllm_paged_batch(n, n_rows, width, width, rs, tab))
+        n = row_start.numel() - 1
+        width = page_table.shape[-1]
+        return n, C.byref(abi.dllm_paged_batch(
+            n, n_rows, width, width, _ints(row_start, "row_start", (n + 1,), self._index),
+            _ints(page_table, "page_table", (n, width), self._index)))
 
     # ------------------------------------------------------------------ calls
     def append(self, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
@@ -112,9 +115,9 @@ class PagedKV:
 
         Rows [row_start[s], row_start[s+1]) go to positions pos[s].. of sequence s, rotated by
         position + rope_shift[s]; page_table [n_seqs][pages] lists each sequence's pages."""
-        rows = k.shape[0]
+        rows, index = k.shape[0], self._index
         n, bt = self._batch(rows, row_start, page_table)
-        heads = qp = qo = None
+        heads, qp, qo = 0, None, None
         if q is not None:
             if q_out is None:
                 q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -123,11 +126,10 @@ class PagedKV:
             qo = self._rows(q_out, "q_out", rows, heads)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        self._call("paged_append", abi.lib().dllm_paged_append, self._kv_p, bt, heads or 0, qp,
+        self._call("paged_append", self._append, self._kv_p, bt, heads, qp,
                    self._rows(k, "k", rows, self.n_kv_heads),
-                   self._rows(v, "v", rows, self.n_kv_heads), qo,
-                   _ints(pos, "pos", (n,), self.device),
-                   None if rope_shift is None else _ints(rope_shift, "rope_shift", (n,), self.device),
+                   self._rows(v, "v", rows, self.n_kv_heads), qo, _ints(pos, "pos", (n,), index),
+                   None if rope_shift is None else _ints(rope_shift, "rope_shift", (n,), index),
                    rope_theta, self._ws_p)
         return q_out
 
@@ -141,14 +143,14 @@ class PagedKV:
                               device=self.device)
         lp = None
         if lse is not None:
-            if lse.dtype != torch.float32 or lse.shape != (rows, self.n_q_heads) \
-                    or lse.device != self.device or not lse.is_contiguous():
+            if lse.dtype is not torch.float32 or lse.shape != (rows, self.n_q_heads) \
+                    or lse.get_device() != self._index or not lse.is_contiguous():
                 raise ValueError(f"lse: a contiguous float32 tensor [{rows}][{self.n_q_heads}] on "
                                  f"{self.device} is needed")
             lp = lse.data_ptr()
-        return out, bt, (_ints(segs, "segs", (n, 2, 2), self.device),
+        return out, bt, (_ints(segs, "segs", (n, 2, 2), self._index),
                          None if row_limit is None
-                         else _ints(row_limit, "row_limit", (rows,), self.device)), \
+                         else _ints(row_limit, "row_limit", (rows,), self._index)), \
             (self._rows(q, "q", rows, self.n_q_heads), self._rows(out, "out", rows, self.n_q_heads),
              lp, self._ws_p, self.ws_bytes)
 
@@ -163,8 +165,7 @@ class PagedKV:
         row_limit int32 [rows]: a row sees only positions below it.  Rows of no sequence are
         left as they were (undefined in a fresh out)."""
         out, bt, keys, rest = self._attn_args(q, row_start, page_table, segs, row_limit, out, lse)
-        self._call("paged_attn", abi.lib().dllm_paged_attn, self._kv_p, bt, self.n_q_heads, *keys,
-                   scale, *rest)
+        self._call("paged_attn", self._attn, self._kv_p, bt, self.n_q_heads, *keys, scale, *rest)
         return out
 
     def shared_prefix_attn(self, q: torch.Tensor, row_start: torch.Tensor,
@@ -177,20 +178,20 @@ class PagedKV:
         group_start[g+1]) also see the prefix_len[g] positions of the pages in
         prefix_table[g]."""
         out, bt, keys, rest = self._attn_args(q, row_start, page_table, segs, row_limit, out, lse)
-        n = group_start.shape[0] - 1 if group_start.dim() == 1 else 0
+        n, index = group_start.numel() - 1, self._index
         if n < 1 or n > self.max_groups:
             raise ValueError(f"{n} prefix groups: this PagedKV was made for 1 to {self.max_groups}")
         width = prefix_table.shape[-1]
         g = abi.dllm_prefix_groups(n, width, width,
-                                   _ints(group_start, "group_start", (n + 1,), self.device),
-                                   _ints(prefix_table, "prefix_table", (n, None), self.device),
-                                   _ints(prefix_len, "prefix_len", (n,), self.device))
-        self._call("shared_prefix_attn", abi.lib().dllm_shared_prefix_attn, self._kv_p, bt,
-                   C.byref(g), self.n_q_heads, *keys, scale, *rest)
+                                   _ints(group_start, "group_start", (n + 1,), index),
+                                   _ints(prefix_table, "prefix_table", (n, width), index),
+                                   _ints(prefix_len, "prefix_len", (n,), index))
+        self._call("shared_prefix_attn", self._shared, self._kv_p, bt, C.byref(g), self.n_q_heads,
+                   *keys, scale, *rest)
         return out
 
     def device_status(self) -> int:
         """The workspace's status word (waits for the current stream)."""
         code = C.c_int32(0)
-        self._call("device_status", abi.lib().dllm_device_status, self._ws_p, C.byref(code))
+        self._call("device_status", self._status, self._ws_p, C.byref(code))
         return int(code.value)
