@@ -435,7 +435,9 @@ DLLM_DEV int block_before(int v, int* scratch, int warp, int lane) {
   return before;
 }
 
-template <int D, bool F16, int MODE>
+// GROUPS: whether there are shared prefixes (a launch's first pass through its code
+// is slow enough for the rest to be left out).
+template <int D, bool F16, int MODE, bool GROUPS>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap,
@@ -526,31 +528,50 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     for (int i = t; i <= n_seqs; i += kAttnThreads)
       rs[i] = min(max(p.bt.row_start[i], 0), p.bt.n_rows);
+    if constexpr (GROUPS) {
+      for (int i = t; i <= p.n_groups; i += kAttnThreads) {
+        const int first = p.gseq[i];
+        if (i < p.n_groups) pk[i] = prefix_keys(p, i);
+        gs[i] = min(max(first, 0), n_seqs);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
       kt[j] = seg_tiles(make_segs(p, raw[j][0], raw[j][1], raw[j][2], raw[j][3]));
-    if (p.n_groups > 0) {
-      for (int i = t; i <= p.n_groups; i += kAttnThreads) gs[i] = min(max(p.gseq[i], 0), n_seqs);
-      for (int i = t; i < p.n_groups; i += kAttnThreads) pk[i] = prefix_keys(p, i);
-      for (int i = t; i < n_seqs; i += kAttnThreads) gid[i] = -1;
-    }
     __syncthreads();
     bool bad = false;
     for (int i = t; i < n_seqs; i += kAttnThreads) bad |= rs[i + 1] < rs[i];
-    for (int i = t; i < p.n_groups; i += kAttnThreads) bad |= gs[i + 1] < gs[i];
+    if constexpr (GROUPS)
+      for (int i = t; i < p.n_groups; i += kAttnThreads) bad |= gs[i + 1] < gs[i];
     if (__syncthreads_or(bad)) {
       if (t == 0) {
         for (int i = 0; i < n_seqs; ++i) rs[i + 1] = max(rs[i + 1], rs[i]);
-        for (int i = 0; i < p.n_groups; ++i) gs[i + 1] = max(gs[i + 1], gs[i]);
+        if constexpr (GROUPS)
+          for (int i = 0; i < p.n_groups; ++i) gs[i + 1] = max(gs[i + 1], gs[i]);
       }
       __syncthreads();
     }
     int* scratch = reinterpret_cast<int*>(x_s);
     int* opfx = reinterpret_cast<int*>(k_s);  // own key tiles of earlier sequences
-    if (p.n_groups > 0) {
-      for (int g = t; g < p.n_groups; g += kAttnThreads)
-        if (pk[g] > 0)
-          for (int i = gs[g]; i < gs[g + 1]; ++i) gid[i] = (short)g;
+    int gr[kPer];  // the group of each sequence, or -1
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) gr[j] = -1;
+    if constexpr (GROUPS) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = t * per + j;
+        if (j >= per || i >= n_seqs) continue;
+        int lo = 0, hi = p.n_groups;  // the last group that starts at or before i
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (gs[mid] <= i)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        if (gs[lo] <= i && i < gs[lo + 1] && pk[lo] > 0) gr[j] = lo;
+        gid[i] = (short)gr[j];
+      }
       int own[kPer], sum = 0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -578,11 +599,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int i = t * per + j;
       units[j] = 0;
       if (j < per && i < n_seqs) {
-        const int g = p.n_groups > 0 ? gid[i] : -1;
+        const int g = gr[j];
         if (g < 0) {
           const int nt = (rs[i + 1] - rs[i] + tile_rows - 1) / tile_rows;
           units[j] = nt * p.kv.Hkv * (max(kt[j], 1) + kTileCost);
-        } else if (i == gs[g]) {
+        } else if (GROUPS && i == gs[g]) {
           const int nt = (rs[gs[g + 1]] - rs[i] + tile_rows - 1) / tile_rows;
           const int own = opfx[gs[g + 1]] - opfx[i];
           if (nt > 0)
@@ -636,7 +657,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint8_t* ring = k_side ? k_s : v_s;
     uint64_t* full = k_side ? k_full : v_full;
     uint64_t* empty = k_side ? k_empty : v_empty;
-    const int places = k_side ? STK : STV;
     bool ok = true, first_piece = true;
     const int page_boxes = max(1, kKeyTile >> p.kv.page_shift);
     const int slot_mask = (1 << p.kv.page_shift) - 1;
@@ -644,7 +664,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     while (ok && u < u1) {
       while (u >= upfx[i + 1]) ++i;
       // ---- the query tile at u
-      const int g = p.n_groups > 0 ? gid[i] : -1;
+      const int g = GROUPS ? gid[i] : -1;
       const int seq_end = g >= 0 ? gs[g + 1] : i + 1;
       const int item_r0 = rs[i], item_r1 = rs[seq_end];
       const int nt = (item_r1 - item_r0 + tile_rows - 1) / tile_rows;
@@ -658,14 +678,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int r0 = item_r0 + (tile - kvh * nt) * tile_rows;
       const int nrows = min(tile_rows, item_r1 - r0);
       int sb = i;  // the sequence of the first row
-      for (int e = seq_end; e - sb > 1;) {
-        const int mid = (sb + e) / 2;
-        if (rs[mid] <= r0)
-          sb = mid;
-        else
-          e = mid;
+      if constexpr (GROUPS) {
+        for (int e = seq_end; e - sb > 1;) {
+          const int mid = (sb + e) / 2;
+          if (rs[mid] <= r0)
+            sb = mid;
+          else
+            e = mid;
+        }
       }
-      // 32 sequences at a time: each lane holds one's segments and key tiles
+      // with groups 32 sequences at a time: each lane holds one's segments and tiles
       const int s_first = sb;
       Segs sg{0, 0, 0, 0};
       int kt = 0, incl = 0, own_before = 0;
@@ -681,15 +703,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (lane >= o) incl += x;
         }
       };
-      load_chunk();
-      int own_total = __shfl_sync(0xffffffffu, incl, 31);
+      int own_total;
+      if constexpr (GROUPS) {
+        load_chunk();
+        own_total = __shfl_sync(0xffffffffu, incl, 31);
+      } else {
+        sg = seq_segs(p, i);
+        own_total = seg_tiles(sg);
+      }
       if (p.row_limit != nullptr && rs[s_first + 1] >= r0 + nrows) {
         // all rows of one sequence: its last tiles may be beyond every row's limit
         int lim = 0;
         for (int r = lane; r < nrows; r += 32) lim = max(lim, p.row_limit[r0 + r]);
         lim = __reduce_max_sync(0xffffffffu, lim);
-        const Segs s0{__shfl_sync(0xffffffffu, sg.a0, 0), __shfl_sync(0xffffffffu, sg.e0, 0),
-                      __shfl_sync(0xffffffffu, sg.a1, 0), __shfl_sync(0xffffffffu, sg.e1, 0)};
+        Segs s0 = sg;
+        if constexpr (GROUPS)
+          s0 = Segs{__shfl_sync(0xffffffffu, sg.a0, 0), __shfl_sync(0xffffffffu, sg.e0, 0),
+                    __shfl_sync(0xffffffffu, sg.a1, 0), __shfl_sync(0xffffffffu, sg.e1, 0)};
         while (own_total > 0) {
           int kb, kl, kh;
           key_tile(s0, own_total - 1, kb, kl, kh);
@@ -697,14 +727,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           --own_total;
         }
       }
-      while (sb + 32 < seq_end && rs[sb + 32] < r0 + nrows) {
-        sb += 32;
-        load_chunk();
-        own_total += __shfl_sync(0xffffffffu, incl, 31);
-      }
-      if (sb != s_first) {
-        sb = s_first;
-        load_chunk();
+      if constexpr (GROUPS) {
+        while (sb + 32 < seq_end && rs[sb + 32] < r0 + nrows) {
+          sb += 32;
+          load_chunk();
+          own_total += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (sb != s_first) {
+          sb = s_first;
+          load_chunk();
+        }
       }
       const int ktp = g >= 0 ? key_tiles(0, pk[g]) : 0;
       const int total = ktp + own_total, allot = cost - kTileCost;
@@ -760,11 +792,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // key tile k of the list, and this lane's page of it (n_pages: nothing to read)
       auto locate = [&](int k) {
         Loc c;
-        Segs x{0, 0, 0, 0};
-        const int* table;
+        Segs x = sg;
+        const int* table = p.bt.table + (size_t)i * p.bt.table_stride;
         int kk = k;
-        if (k < ktp) {
-          x.e0 = pk[g];
+        if constexpr (!GROUPS) {
+          c.w = nrows << 9 | 1 << 18;
+        } else if (k < ktp) {
+          x = Segs{0, pk[g], 0, 0};
           table = p.ptable + (size_t)g * p.ptable_stride;
           c.w = nrows << 9;
         } else {
@@ -801,7 +835,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int j = 0; ok && j < n; ++j) {
         Loc next = c;
         if (j + 1 < n) next = locate(k0 + j + 1);
-        const int ti = n_tile + j, round = (unsigned)ti / (unsigned)places, st = ti - round * places;
+        const int ti = n_tile + j;
+        const int round = k_side ? ti / STK : ti / STV, st = k_side ? ti % STK : ti % STV;
         if (lane == 0) {
           ok = round == 0 || wait_or_abort(&empty[st], (round - 1) & 1, p.status, abort);
           if (ok) mbar_arrive_expect_tx(&full[st], C::kTile);
@@ -1342,11 +1377,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// Block (c, y) merges elements 8y.. 8y + 7 of the rows of the cut query tile that
-// starts in CTA c of the attention kernel: its parts are in that CTA's slot and in
-// the even slots of the CTAs after it.  A lane takes a row, a warp 32 rows; where a
-// tile has fewer rows, several warps share its parts.
-constexpr int kMergeWarps = 8;
+// The cut query tiles of a launch are those that the CTAs recorded.  Every block
+// gathers them in shared memory; then all warps of the grid share the work: an item
+// is eight elements of 32 rows of a tile (a lane a row, as the parts are stored), and
+// where there are fewer items than warps, several warps share an item's parts.  The
+// parts of a tile are in the slot of the CTA it starts in and in the even slots of
+// the CTAs after it; they are added in that order.  One resident wave of blocks: a
+// grid with blocks for every CTA that mostly find nothing took 2 to 5 us more.
+constexpr int kMergeWarps = 8, kMergeBlocks = 4 * kNumSMs;
 
 struct RowSum {
   float m = -FLT_MAX, l = 0.f, o[8] = {};
@@ -1363,69 +1401,93 @@ struct RowSum {
 };
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kMergeWarps * 32)
+__global__ void __launch_bounds__(kMergeWarps * 32, 4)
     paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
+  __shared__ int4 tiles[kNumSMs];  // first row, rows | kv head << 12, parts, first slot
+  __shared__ int counts[kMergeWarps];
   __shared__ float2 ml_s[kMergeWarps][32];
   __shared__ float4 o_s[kMergeWarps][2][32];
+  static_assert(kNumSMs <= kMergeWarps * 32, "a thread for each record");
   grid_dep_wait();
   grid_dep_launch();
-  const int4 cut = p.cut[blockIdx.x];  // first row, rows, kv head, parts | slot parity << 16
-  const int parts = cut.w & 0xffff, slot0 = 2 * blockIdx.x + (cut.w >> 16);
-  if (parts < 2) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // places of the slot in use: 256-row tiles have 128 for each half
-  const int places = cut.y > p.rows_per_tile ? 128 + (cut.y - p.rows_per_tile) * p.G : cut.y * p.G;
-  const int warps = (places + 31) / 32;  // 1 to 8
-  const int split = warps > 4 ? 1 : warps > 2 ? 2 : warps > 1 ? 4 : 8;
-  const int wrow = warp / split, wpart = warp - wrow * split;
-  const int at = wrow * 32 + lane;
-  const int half = at >> 7, in = at & 127;
-  const int rr = in / p.G + half * p.rows_per_tile, hh = in % p.G;
-  const bool have = at < places && in < p.rows_per_tile * p.G && rr < cut.y;
-  RowSum sum;
-  if (have) {
-    const float4* part = reinterpret_cast<const float4*>(p.part) + 2 * blockIdx.y * p.slot_rows + at;
-    constexpr int kUn = 4;
-    for (int i = wpart; i < parts; i += kUn * split) {
-      float2 ml[kUn];
-      float4 x[kUn], y[kUn];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int4 cut = t < kNumSMs ? p.cut[t] : make_int4(0, 0, 0, 0);
+  const bool is = (cut.w & 0xffff) > 1;
+  const unsigned mask = __ballot_sync(0xffffffffu, is);
+  if (lane == 0) counts[warp] = __popc(mask);
+  __syncthreads();
+  int before = __popc(mask & ((1u << lane) - 1)), n = 0;
 #pragma unroll
-      for (int k = 0; k < kUn; ++k) {
-        const int ip = i + k * split;
-        ml[k] = make_float2(-FLT_MAX, 0.f);
-        if (ip < parts) {
-          const size_t ro = (size_t)(ip == 0 ? slot0 : 2 * (blockIdx.x + ip)) * p.slot_rows;
-          ml[k] = p.part_ml[ro + at];
-          x[k] = part[ro * (D / 4)];
-          y[k] = part[ro * (D / 4) + p.slot_rows];
+  for (int w = 0; w < kMergeWarps; ++w) {
+    if (w < warp) before += counts[w];
+    n += counts[w];
+  }
+  if (n == 0) return;
+  if (is)
+    tiles[before] =
+        make_int4(cut.x, cut.y | cut.z << 12, cut.w & 0xffff, 2 * t + (cut.w >> 16));
+  __syncthreads();
+  const int rows32 = (p.slot_rows + 31) / 32;  // warps for the rows of a tile
+  const int per_tile = D / 8 * rows32;
+  const int items = n * per_tile, warps = gridDim.x * kMergeWarps;
+  const int split = items * 8 <= warps ? 8 : items * 4 <= warps ? 4 : items * 2 <= warps ? 2 : 1;
+  const int wpart = warp % split;
+  for (int i0 = blockIdx.x * (kMergeWarps / split); i0 < items; i0 += warps / split) {
+    const int item = i0 + warp / split;
+    const int ti = min(item / per_tile, n - 1), in_tile = item - ti * per_tile;
+    const int4 tile = tiles[ti];
+    const int col8 = in_tile / rows32;
+    const int at = (in_tile - col8 * rows32) * 32 + lane;
+    // 256-row tiles have 128 places for each half
+    const int half = at >> 7, in = at & 127;
+    const int rr = in / p.G + half * p.rows_per_tile, hh = in % p.G;
+    const bool have = item < items && in < p.rows_per_tile * p.G && rr < (tile.y & 0xfff);
+    RowSum sum;
+    if (have) {
+      const float4* part = reinterpret_cast<const float4*>(p.part) + 2 * col8 * p.slot_rows + at;
+      constexpr int kUn = 2;
+      for (int i = wpart; i < tile.z; i += kUn * split) {
+        float2 ml[kUn];
+        float4 x[kUn], y[kUn];
+#pragma unroll
+        for (int k = 0; k < kUn; ++k) {
+          const int ip = i + k * split;
+          ml[k] = make_float2(-FLT_MAX, 0.f);
+          if (ip < tile.z) {
+            const size_t ro =
+                (size_t)(ip == 0 ? tile.w : (tile.w & ~1) + 2 * ip) * p.slot_rows;
+            ml[k] = p.part_ml[ro + at];
+            x[k] = part[ro * (D / 4)];
+            y[k] = part[ro * (D / 4) + p.slot_rows];
+          }
         }
-      }
 #pragma unroll
-      for (int k = 0; k < kUn; ++k) sum.join(ml[k], x[k], y[k]);
+        for (int k = 0; k < kUn; ++k) sum.join(ml[k], x[k], y[k]);
+      }
     }
-  }
-  if (split > 1) {
-    ml_s[warp][lane] = make_float2(sum.m, sum.l);
-    o_s[warp][0][lane] = make_float4(sum.o[0], sum.o[1], sum.o[2], sum.o[3]);
-    o_s[warp][1][lane] = make_float4(sum.o[4], sum.o[5], sum.o[6], sum.o[7]);
-    __syncthreads();
-    if (wpart == 0)
-      for (int w = warp + 1; w < warp + split; ++w)
-        sum.join(ml_s[w][lane], o_s[w][0][lane], o_s[w][1][lane]);
-  }
-  if (have && wpart == 0) {
-    const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
-    const int r = cut.x + rr, head = cut.z * p.G + hh;
-    uint16_t* out =
-        static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride + head * p.out.head_stride;
-    *reinterpret_cast<uint4*>(out + 8 * blockIdx.y) =
-        make_uint4(pack2<F16>(sum.o[0] * inv, sum.o[1] * inv),
-                   pack2<F16>(sum.o[2] * inv, sum.o[3] * inv),
-                   pack2<F16>(sum.o[4] * inv, sum.o[5] * inv),
-                   pack2<F16>(sum.o[6] * inv, sum.o[7] * inv));
-    if (blockIdx.y == 0 && p.lse != nullptr)
-      p.lse[(size_t)r * p.Hq + head] =
-          sum.l > 0.f ? 0.6931471805599453f * sum.m + logf(sum.l) : -INFINITY;
+    if (split > 1) {  // (then there is one round)
+      ml_s[warp][lane] = make_float2(sum.m, sum.l);
+      o_s[warp][0][lane] = make_float4(sum.o[0], sum.o[1], sum.o[2], sum.o[3]);
+      o_s[warp][1][lane] = make_float4(sum.o[4], sum.o[5], sum.o[6], sum.o[7]);
+      __syncthreads();
+      if (wpart == 0)
+        for (int k = 1; k < split; ++k)
+          sum.join(ml_s[warp + k][lane], o_s[warp + k][0][lane], o_s[warp + k][1][lane]);
+    }
+    if (have && wpart == 0) {
+      const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
+      const int r = tile.x + rr, head = (tile.y >> 12) * p.G + hh;
+      uint16_t* out =
+          static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride + head * p.out.head_stride;
+      *reinterpret_cast<uint4*>(out + 8 * col8) =
+          make_uint4(pack2<F16>(sum.o[0] * inv, sum.o[1] * inv),
+                     pack2<F16>(sum.o[2] * inv, sum.o[3] * inv),
+                     pack2<F16>(sum.o[4] * inv, sum.o[5] * inv),
+                     pack2<F16>(sum.o[6] * inv, sum.o[7] * inv));
+      if (col8 == 0 && p.lse != nullptr)
+        p.lse[(size_t)r * p.Hq + head] =
+            sum.l > 0.f ? 0.6931471805599453f * sum.m + logf(sum.l) : -INFINITY;
+    }
   }
 }
 
@@ -1434,8 +1496,12 @@ namespace {
 template <int D, bool F16, int MODE>
 cudaError_t launch_mode(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
                         const PagedAttnParams& p, cudaStream_t s) {
-  return launch_pdl(paged_attn_kernel<D, F16, MODE>, dim3(kNumSMs), dim3(kAttnThreads),
-                    PagedCfg<D, MODE>::kSmem, s, qm, km, vm, p);
+  const dim3 grid(kNumSMs), block(kAttnThreads);
+  constexpr size_t smem = PagedCfg<D, MODE>::kSmem;
+  return p.n_groups > 0 ? launch_pdl(paged_attn_kernel<D, F16, MODE, true>, grid, block, smem, s,
+                                     qm, km, vm, p)
+                        : launch_pdl(paged_attn_kernel<D, F16, MODE, false>, grid, block, smem,
+                                     s, qm, km, vm, p);
 }
 
 template <int D, bool F16>
@@ -1445,7 +1511,7 @@ cudaError_t launch_paged_attn_t(const CUtensorMap& qm, const CUtensorMap& km, co
                         : mode == kQuad ? launch_mode<D, F16, kQuad>(qm, km, vm, p, s)
                                         : launch_mode<D, F16, kSplit>(qm, km, vm, p, s);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_merge_kernel<D, F16>, dim3(kNumSMs, D / 8), dim3(kMergeWarps * 32), 0, s,
+  return launch_pdl(paged_merge_kernel<D, F16>, dim3(kMergeBlocks), dim3(kMergeWarps * 32), 0, s,
                     p);
 }
 
@@ -1455,9 +1521,12 @@ cudaError_t prepare_mode() {
   static_assert(PagedCfg<D, MODE>::kSTK >= 2 && PagedCfg<D, MODE>::kSTK <= 6 &&
                     PagedCfg<D, MODE>::kSTV >= 2,
                 "see the key tile queue");
-  return cudaFuncSetAttribute(paged_attn_kernel<D, F16, MODE>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)PagedCfg<D, MODE>::kSmem);
+  constexpr int smem = (int)PagedCfg<D, MODE>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, F16, MODE, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(paged_attn_kernel<D, F16, MODE, true>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 template <int D, bool F16>

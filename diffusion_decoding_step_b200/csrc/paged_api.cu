@@ -172,7 +172,7 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
   p.slot_rows = slot_rows(p.bt.n_rows, p.G);
   if (ws_bytes < workspace_bytes(p.kv, p.slot_rows)) return DLLM_ERR_WORKSPACE;
   const int mode = query_tiles(p.bt.n_rows, groups ? p.n_groups : p.bt.n_seqs, p.G);
-  if (mode == kPagedQuad) p.slot_rows = std::min(p.slot_rows, 32);
+  p.slot_rows = std::min(p.slot_rows, mode == kPagedQuad ? 32 : mode == kPagedSplit ? 128 : 256);
   const int D = p.kv.D;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.rows_per_tile = (mode == kPagedQuad ? 32 : 128) / p.G;
