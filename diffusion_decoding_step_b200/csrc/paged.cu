@@ -888,6 +888,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ++n_piece;
         if (n < 0) break;
         if (n == 0) continue;
+        // A poll takes some 60 ns even when it succeeds: those whose outcome is likely
+        // are made before a run of products and looked at behind it.
+        auto poll_k = [&](int j) {
+          const int ti = n_tile + j;
+          return mbar_try_wait(&k_full[ti % STK], (ti / STK) & 1);
+        };
+        auto poll_v = [&](int j) {
+          const int ti = n_tile + j;
+          return mbar_try_wait(&v_full[ti % STV], (ti / STV) & 1);
+        };
         auto wait_k = [&](int j) {
           const int ti = n_tile + j;
           return wait_or_abort(&k_full[ti % STK], (ti / STK) & 1, p.status, abort);
@@ -896,6 +906,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int ti = n_tile + j;
           return wait_or_abort(&v_full[ti % STV], (ti / STV) & 1, p.status, abort);
         };
+        auto poll_p = [&](int x) { return mbar_try_wait(&p_full[x], n_p[x] & 1); };
         // S of key tile j in stream x; after the last use K (and Q) are free
         auto s_mma = [&](int x, int j, bool last) {
           const int st = (n_tile + j) % STK;
@@ -915,7 +926,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         };
         // O of stream x.  128-key rows have the second half of P ready first: where
         // the whole is not there yet, its products start.
-        auto pv_mma = [&](int x, int j, bool accumulate, bool last) {
+        auto pv_mma = [&](int x, int j, bool accumulate, bool last, bool whole) {
           const int st = (n_tile + j) % STV;
           const uint64_t vd = v_desc + (uint64_t)(st * C::kTile >> 4);
           constexpr int kSteps = kKeyTile / 16;
@@ -927,12 +938,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                           vd + ((from + k) * 16 * C::kRowBytes >> 4), kIdO, acc || k > 0);
           };
           const uint32_t parity = n_p[x]++ & 1;
-          const bool whole = QUAD || mbar_try_wait(&p_full[x], parity);
-          if (!wait_or_abort(whole ? &p_full[x] : &p_half[x], parity, p.status, abort))
+          if (!whole &&
+              !wait_or_abort(QUAD ? &p_full[x] : &p_half[x], parity, p.status, abort))
             return false;
           tc_fence_after();
           steps(kSteps / 2, accumulate);
-          if (!whole) {
+          if (!QUAD && !whole) {
             if (!wait_or_abort(&p_full[x], parity, p.status, abort)) return false;
             tc_fence_after();
           }
@@ -947,14 +958,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           s_mma(0, 0, !two);
           if (two) s_mma(1, 0, true);
           ok = n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort);
+          bool v_there = poll_v(0), p_there = poll_p(0);
           for (int j = 0; ok && j < n; ++j) {
-            ok = wait_v(j) && pv_mma(0, j, j > 0, !two) && (j + 1 >= n || wait_k(j + 1));
+            const bool more = j + 1 < n;
+            ok = v_there || wait_v(j);
+            if (!ok) break;
+            const bool k_there = more && poll_k(j + 1);
+            ok = pv_mma(0, j, j > 0, !two, p_there) && (k_there || !more || wait_k(j + 1));
             if (!ok) break;
             tc_fence_after();
-            if (j + 1 < n) s_mma(0, j + 1, !two);
+            p_there = two && poll_p(1);
+            if (more) s_mma(0, j + 1, !two);
+            v_there = more && poll_v(j + 1);
             if (two) {
-              ok = pv_mma(1, j, j > 0, true);
-              if (ok && j + 1 < n) s_mma(1, j + 1, true);
+              ok = pv_mma(1, j, j > 0, true, p_there);
+              p_there = more && poll_p(0);
+              if (ok && more) s_mma(1, j + 1, true);
+            } else {
+              p_there = more && poll_p(0);
             }
           }
         } else {
@@ -965,12 +986,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             s_mma(b ^ 1, 1, true);
           }
           ok = ok && (n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort));
+          bool v_there = poll_v(0), p_there = poll_p(b);
           for (int j = 0; ok && j < n; ++j) {
-            ok = wait_v(j) && pv_mma((b + j) & 1, j, j > 1, true);
-            if (ok && j + 2 < n && (ok = wait_k(j + 2))) {
-              tc_fence_after();
-              s_mma((b + j) & 1, j + 2, true);
-            }
+            const bool more = j + 2 < n;
+            ok = v_there || wait_v(j);
+            if (!ok) break;
+            const bool k_there = more && poll_k(j + 2);
+            ok = pv_mma((b + j) & 1, j, j > 1, true, p_there) &&
+                 (k_there || !more || wait_k(j + 2));
+            if (!ok) break;
+            tc_fence_after();
+            v_there = j + 1 < n && poll_v(j + 1);
+            p_there = j + 1 < n && poll_p((b + j + 1) & 1);
+            if (more) s_mma((b + j) & 1, j + 2, true);
           }
         }
         if (ok) umma_commit(o_full);

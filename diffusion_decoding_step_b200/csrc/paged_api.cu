@@ -88,11 +88,11 @@ dllm_status check_heads(int n_q_heads, const PagedPool& kv) {
 
 // Query tiles by the average query rows of an item (a group, or a sequence
 // without one), rounded down since a padded batch has a few rows too many: up to
-// 32 rows the 32-row tiles, whose softmax is spread over all warps; above 128 the
-// 256-row ones, whose halves share every key tile.
+// 32 rows the 32-row tiles, whose softmax is spread over all warps; well above 128
+// the 256-row ones, whose halves share every key tile.
 int query_tiles(int n_rows, int items, int G) {
   const long long rows = (long long)std::max(n_rows / items, 1) * G;
-  return rows <= 32 ? kPagedQuad : rows > 128 ? kPagedPair : kPagedSplit;
+  return rows <= 32 ? kPagedQuad : rows > 144 ? kPagedPair : kPagedSplit;
 }
 
 // Workspace: status word, a record per CTA, the parts of cut query tiles.
