@@ -400,21 +400,26 @@ DLLM_DEV void trade_units(uint4 (&u)[N], int lane) {
   }
 }
 
-// A wait that ends when another role gave up; sets the flag when it gives up itself.
-DLLM_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0u) {
-      if (*abort) return false;
-      if (global_ns() - t0 > kWaitLimitNs) {
-        *abort = 1;
-        if (status) atomicOr(status, kErrTimeout);
-        return false;
-      }
+// A whole warp waits; false when it or another role gave up, which sets the flag.
+DLLM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  bool ok = true;
+  unsigned long long t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 63u) != 0u) continue;
+    if (*abort) {
+      ok = false;
+      break;
+    }
+    const unsigned long long now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      *abort = 1;
+      if (status) atomicOr(status, kErrTimeout);
+      ok = false;
+      break;
     }
   }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // Sum over the block's threads before this one (all threads; scratch of one
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_empty + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int t = threadIdx.x, warp = uniform(t >> 5), lane = t & 31;
   const int tile_rows = p.rows_per_tile * C::kQ;
   if (t == 0) {
     for (int i = 0; i < STK; ++i) {
@@ -491,18 +496,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 257);
+      mbar_init(&d_empty[i], 9);  // a lane of each warp that reads it
     }
     for (int i = 0; i < kTileQueue; ++i) mbar_init(&t_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_half[i], 128);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_half[i], 4);  // a lane of each warp of the stream
+      mbar_init(&p_full[i], 4);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(o_full, 1);
-    mbar_init(o_empty, 256);
+    mbar_init(o_empty, 8);
     *abort = 0;
     fence_barrier_init();
     prefetch_tmap(&qmap);
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   grid_dep_launch();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
 
   if (warp == 8 || warp == 10) {
     // ================================================================ producers
@@ -657,6 +662,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint8_t* ring = k_side ? k_s : v_s;
     uint64_t* full = k_side ? k_full : v_full;
     uint64_t* empty = k_side ? k_empty : v_empty;
+    const CUtensorMap* map = k_side ? &kmap : &vmap;
     bool ok = true, first_piece = true;
     const int page_boxes = max(1, kKeyTile >> p.kv.page_shift);
     const int slot_mask = (1 << p.kv.page_shift) - 1;
@@ -749,29 +755,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
       // ---- its description
       const int qi = n_piece % kQueue;
-      if (k_side && lane == 0) {
+      if (k_side) {
         ok = n_piece < kQueue ||
-             wait_or_abort(&d_empty[qi], (n_piece / kQueue - 1) & 1, p.status, abort);
-        if (ok) {
+             warp_wait(&d_empty[qi], (n_piece / kQueue - 1) & 1, p.status, abort);
+        if (ok && lane == 0) {
           Piece d{r0, nrows, kvh, n, 1, 2 * cta + (first_piece ? 0 : 1)};
           if (x0 > start + kTileCost || x1 < end) {
             d.parts = sh.owner(end - 1) - sh.owner(start + kTileCost) + 1;
             if (x0 == start + kTileCost)
-              cut = make_int4(r0, nrows, kvh, d.parts | (d.slot & 1) << 16);
+              cut = make_int4(r0, nrows, kvh, d.parts | (d.slot & 1) << 16);  // (lane 0's)
           }
           queue[qi] = d;
           mbar_arrive(&d_full[qi]);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       ++n_piece;
       first_piece = false;
       if (!ok || n == 0) continue;
 
       // ---- its loads
-      if (k_side && lane == 0) {
-        ok = n_q == 0 || wait_or_abort(q_empty, (n_q - 1) & 1, p.status, abort);
-        if (ok) {
+      if (k_side) {
+        ok = n_q == 0 || warp_wait(q_empty, (n_q - 1) & 1, p.status, abort);
+        const int q_row = uniform(r0), q_head = uniform(kvh) * p.G;
+        if (ok && elect_one()) {
           constexpr int kCopies = QUAD ? 4 : C::kQ;
           mbar_arrive_expect_tx(q_full,
                                 kCopies * C::kNBox * p.G * p.rows_per_tile * C::kRowBytes);
@@ -780,12 +786,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
             for (int b = 0; b < C::kNBox; ++b)
               tma_load_3d(q_s + h * (QUAD ? 32 * C::kRowBytes : C::kTile) + b * C::kBoxBytes,
-                          &qmap, q_full, b * C::kBoxD, kvh * p.G,
-                          r0 + (QUAD ? 0 : h * p.rows_per_tile));
+                          &qmap, q_full, b * C::kBoxD, q_head,
+                          q_row + (QUAD ? 0 : h * p.rows_per_tile));
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       ++n_q;
+
       struct Loc {
         int kb, kl, kh, w, page;
       };
@@ -836,19 +842,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         Loc next = c;
         if (j + 1 < n) next = locate(k0 + j + 1);
         const int ti = n_tile + j;
-        const int round = k_side ? ti / STK : ti / STV, st = k_side ? ti % STK : ti % STV;
-        if (lane == 0) {
-          ok = round == 0 || wait_or_abort(&empty[st], (round - 1) & 1, p.status, abort);
-          if (ok) mbar_arrive_expect_tx(&full[st], C::kTile);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        const int round = k_side ? ti / STK : ti / STV;
+        const int st = uniform(k_side ? ti % STK : ti % STV);
+        ok = round == 0 || warp_wait(&empty[st], (round - 1) & 1, p.status, abort);
         if (!ok) break;
-        if (lane < page_boxes) {
-          uint8_t* dst = ring + st * C::kTile + lane * page_keys * C::kRowBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTile);
+        const int slot = uniform(page_keys == kKeyTile ? c.kb & slot_mask : 0);
+        const int head = uniform(kvh);
+        uint8_t* dst = ring + st * C::kTile;
+#pragma unroll 1
+        for (int b = 0; b < page_boxes; ++b) {
+          const int page = __shfl_sync(0xffffffffu, c.page, b);
+          if (elect_one()) {
 #pragma unroll
-          for (int b = 0; b < C::kNBox; ++b)
-            tma_load_4d(dst + b * C::kBoxBytes, k_side ? &kmap : &vmap, &full[st],
-                        b * C::kBoxD, page_keys == kKeyTile ? c.kb & slot_mask : 0, kvh, c.page);
+            for (int x = 0; x < C::kNBox; ++x)
+              tma_load_4d(dst + x * C::kBoxBytes, map, &full[st], x * C::kBoxD, slot, head, page);
+          }
+          dst += page_keys * C::kRowBytes;
         }
         if (k_side && lane == 0) {
           tiles_s[ti % kTileQueue] = make_int4(c.kb, c.kl, c.kh, c.w);
@@ -858,18 +868,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       n_tile += n;
     }
-    if (k_side && lane == 0) {
+    if (k_side) {
       const int qi = n_piece % kQueue;
-      if (ok && (n_piece < kQueue ||
-                 wait_or_abort(&d_empty[qi], (n_piece / kQueue - 1) & 1, p.status, abort))) {
-        queue[qi].n = -1;
-        mbar_arrive(&d_full[qi]);
+      ok = ok && (n_piece < kQueue ||
+                  warp_wait(&d_empty[qi], (n_piece / kQueue - 1) & 1, p.status, abort));
+      if (lane == 0) {
+        if (ok) {
+          queue[qi].n = -1;
+          mbar_arrive(&d_full[qi]);
+        }
+        p.cut[cta] = cut;
       }
-      p.cut[cta] = cut;
     }
   } else if (warp == 9) {
     // ================================================================ products
-    if (lane == 0) {
+    {
       constexpr uint32_t kIdS = idesc_16(F16, 128, kKeyTile, 0, 0);
       constexpr uint32_t kIdO = idesc_16(F16, 128, D, 0, 1);
       const uint64_t q_desc = smem_desc(smem_u32(q_s), 16, 8 * C::kRowBytes, C::kSw);
@@ -880,57 +893,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bool ok = true;
       while (ok) {
         const int qi = n_piece % kQueue;
-        ok = wait_or_abort(&d_full[qi], (n_piece / kQueue) & 1, p.status, abort);
+        ok = warp_wait(&d_full[qi], (n_piece / kQueue) & 1, p.status, abort);
         if (!ok) break;
-        const int n = queue[qi].n;
-        const bool two = queue[qi].nrows > p.rows_per_tile;  // rows in both halves
-        mbar_arrive(&d_empty[qi]);
+        const int n = uniform(queue[qi].n);
+        const bool two = uniform(queue[qi].nrows) > p.rows_per_tile;  // rows in both halves
+        if (elect_one()) mbar_arrive(&d_empty[qi]);
         ++n_piece;
         if (n < 0) break;
         if (n == 0) continue;
-        // A poll takes some 60 ns even when it succeeds: those whose outcome is likely
-        // are made before a run of products and looked at behind it.
-        auto poll_k = [&](int j) {
-          const int ti = n_tile + j;
-          return mbar_try_wait(&k_full[ti % STK], (ti / STK) & 1);
-        };
-        auto poll_v = [&](int j) {
-          const int ti = n_tile + j;
-          return mbar_try_wait(&v_full[ti % STV], (ti / STV) & 1);
-        };
         auto wait_k = [&](int j) {
           const int ti = n_tile + j;
-          return wait_or_abort(&k_full[ti % STK], (ti / STK) & 1, p.status, abort);
+          return warp_wait(&k_full[ti % STK], (ti / STK) & 1, p.status, abort);
         };
         auto wait_v = [&](int j) {
           const int ti = n_tile + j;
-          return wait_or_abort(&v_full[ti % STV], (ti / STV) & 1, p.status, abort);
+          return warp_wait(&v_full[ti % STV], (ti / STV) & 1, p.status, abort);
         };
-        auto poll_p = [&](int x) { return mbar_try_wait(&p_full[x], n_p[x] & 1); };
         // S of key tile j in stream x; after the last use K (and Q) are free
         auto s_mma = [&](int x, int j, bool last) {
           const int st = (n_tile + j) % STK;
           const uint64_t kd = k_desc + (uint64_t)(st * C::kTile >> 4);
           const uint64_t qd = q_desc + (uint64_t)(PAIR ? x * C::kTile >> 4 : 0);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            constexpr int kPerBox = C::kBoxD / 16;
-            const int off = (kk / kPerBox) * C::kBoxBytes + (kk % kPerBox) * 32;
-            umma_bf16(tmem + x * 128, qd + (off >> 4), kd + (off >> 4), kIdS, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              constexpr int kPerBox = C::kBoxD / 16;
+              const int off = (kk / kPerBox) * C::kBoxBytes + (kk % kPerBox) * 32;
+              umma_bf16(tmem + x * 128, qd + (off >> 4), kd + (off >> 4), kIdS, kk > 0);
+            }
+            umma_commit(&s_full[x]);
+            if (last) {
+              umma_commit(&k_empty[st]);
+              if (j == n - 1) umma_commit(q_empty);
+            }
           }
-          umma_commit(&s_full[x]);
-          if (last) {
-            umma_commit(&k_empty[st]);
-            if (j == n - 1) umma_commit(q_empty);
-          }
+          __syncwarp();
         };
         // O of stream x.  128-key rows have the second half of P ready first: where
         // the whole is not there yet, its products start.
-        auto pv_mma = [&](int x, int j, bool accumulate, bool last, bool whole) {
+        auto pv_mma = [&](int x, int j, bool accumulate, bool last) {
           const int st = (n_tile + j) % STV;
           const uint64_t vd = v_desc + (uint64_t)(st * C::kTile >> 4);
           constexpr int kSteps = kKeyTile / 16;
-          // key steps 4 to 7 and then 0 to 3, whatever is there first
           auto steps = [&](int from, bool acc) {
 #pragma unroll
             for (int k = 0; k < kSteps / 2; ++k)
@@ -938,44 +942,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                           vd + ((from + k) * 16 * C::kRowBytes >> 4), kIdO, acc || k > 0);
           };
           const uint32_t parity = n_p[x]++ & 1;
-          if (!whole &&
-              !wait_or_abort(QUAD ? &p_full[x] : &p_half[x], parity, p.status, abort))
-            return false;
-          tc_fence_after();
-          steps(kSteps / 2, accumulate);
-          if (!QUAD && !whole) {
-            if (!wait_or_abort(&p_full[x], parity, p.status, abort)) return false;
+          if constexpr (!QUAD) {
+            if (!warp_wait(&p_half[x], parity, p.status, abort)) return false;
             tc_fence_after();
+            if (elect_one()) steps(kSteps / 2, accumulate);
+            __syncwarp();
           }
-          steps(0, true);
-          if (last) umma_commit(&v_empty[st]);
+          if (!warp_wait(&p_full[x], parity, p.status, abort)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            if constexpr (QUAD) steps(kSteps / 2, accumulate);
+            steps(0, true);
+            if (last) umma_commit(&v_empty[st]);
+          }
+          __syncwarp();
           return true;
         };
-        ok = wait_or_abort(q_full, n_q & 1, p.status, abort) && wait_k(0);
+        ok = warp_wait(q_full, n_q & 1, p.status, abort) && wait_k(0);
         if (!ok) break;
         tc_fence_after();
         if constexpr (PAIR) {
           s_mma(0, 0, !two);
           if (two) s_mma(1, 0, true);
-          ok = n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort);
-          bool v_there = poll_v(0), p_there = poll_p(0);
+          ok = n_q == 0 || warp_wait(o_empty, (n_q - 1) & 1, p.status, abort);
           for (int j = 0; ok && j < n; ++j) {
             const bool more = j + 1 < n;
-            ok = v_there || wait_v(j);
-            if (!ok) break;
-            const bool k_there = more && poll_k(j + 1);
-            ok = pv_mma(0, j, j > 0, !two, p_there) && (k_there || !more || wait_k(j + 1));
+            ok = wait_v(j) && pv_mma(0, j, j > 0, !two) && (!more || wait_k(j + 1));
             if (!ok) break;
             tc_fence_after();
-            p_there = two && poll_p(1);
             if (more) s_mma(0, j + 1, !two);
-            v_there = more && poll_v(j + 1);
             if (two) {
-              ok = pv_mma(1, j, j > 0, true, p_there);
-              p_there = more && poll_p(0);
+              ok = pv_mma(1, j, j > 0, true);
               if (ok && more) s_mma(1, j + 1, true);
-            } else {
-              p_there = more && poll_p(0);
             }
           }
         } else {
@@ -985,23 +983,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tc_fence_after();
             s_mma(b ^ 1, 1, true);
           }
-          ok = ok && (n_q == 0 || wait_or_abort(o_empty, (n_q - 1) & 1, p.status, abort));
-          bool v_there = poll_v(0), p_there = poll_p(b);
+          ok = ok && (n_q == 0 || warp_wait(o_empty, (n_q - 1) & 1, p.status, abort));
           for (int j = 0; ok && j < n; ++j) {
-            const bool more = j + 2 < n;
-            ok = v_there || wait_v(j);
-            if (!ok) break;
-            const bool k_there = more && poll_k(j + 2);
-            ok = pv_mma((b + j) & 1, j, j > 1, true, p_there) &&
-                 (k_there || !more || wait_k(j + 2));
-            if (!ok) break;
-            tc_fence_after();
-            v_there = j + 1 < n && poll_v(j + 1);
-            p_there = j + 1 < n && poll_p((b + j + 1) & 1);
-            if (more) s_mma((b + j) & 1, j + 2, true);
+            ok = wait_v(j) && pv_mma((b + j) & 1, j, j > 1, true);
+            if (ok && j + 2 < n && (ok = wait_k(j + 2))) {
+              tc_fence_after();
+              s_mma((b + j) & 1, j + 2, true);
+            }
           }
         }
-        if (ok) umma_commit(o_full);
+        if (ok && elect_one()) umma_commit(o_full);
+        __syncwarp();
         n_tile += n;
         ++n_q;
       }
@@ -1020,10 +1012,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bool ok = true;
     while (ok) {
       const int qi = n_piece % kQueue;
-      ok = wait_or_abort(&d_full[qi], (n_piece / kQueue) & 1, p.status, abort);
+      ok = warp_wait(&d_full[qi], (n_piece / kQueue) & 1, p.status, abort);
       if (!ok) break;
-      const Piece d = queue[qi];
-      mbar_arrive(&d_empty[qi]);
+      const Piece d{uniform(queue[qi].r0), uniform(queue[qi].nrows), uniform(queue[qi].kvh),
+                    uniform(queue[qi].n), uniform(queue[qi].parts), uniform(queue[qi].slot)};
+      if (lane == 0) mbar_arrive(&d_empty[qi]);
       ++n_piece;
       if (d.n < 0) break;
       const bool valid = row_in < p.rows_per_tile && rr < d.nrows;
@@ -1055,7 +1048,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int j0 = PAIR ? 0 : (wg ^ n_tile) & 1;  // split: the streams take tiles in turn
       for (int j = j0; stream && j < d.n; j += PAIR ? 1 : 2) {
         const int ti = n_tile + j;
-        ok = wait_or_abort(&t_full[ti % kTileQueue], (ti / kTileQueue) & 1, p.status, abort);
+        ok = warp_wait(&t_full[ti % kTileQueue], (ti / kTileQueue) & 1, p.status, abort);
         if (!ok) break;
         const int4 tl = tiles_s[ti % kTileQueue];  // base, lo, hi, rows
         const bool own = tl.w >> 18;
@@ -1065,7 +1058,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool sees = __any_sync(0xffffffffu, end_k > first_k);
         const bool masked =
             __any_sync(0xffffffffu, valid && (first_k > 0 || end_k < kKeyTile));
-        ok = wait_or_abort(&s_full[wg], s_cnt & 1, p.status, abort);
+        ok = warp_wait(&s_full[wg], s_cnt & 1, p.status, abort);
         if (!ok) break;
         ++s_cnt;
         tc_fence_after();
@@ -1076,7 +1069,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (tl.y > tl.x || tl.z < tl.x + kKeyTile) {
           const int key = tl.x + row;
           const int pg = key & ~(page_keys - 1);
-          ok = wait_or_abort(&v_full[ti % STV], (ti / STV) & 1, p.status, abort);
+          ok = warp_wait(&v_full[ti % STV], (ti / STV) & 1, p.status, abort);
           if (!ok) break;
           if ((key < tl.y || key >= tl.z) && pg < tl.z && pg + page_keys > tl.y) {
             uint4* v = reinterpret_cast<uint4*>(v_s + (ti % STV) * C::kTile + row * C::kRowBytes);
@@ -1097,7 +1090,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           if constexpr (!QUAD) {
             tc_fence_before();
-            mbar_arrive(&p_half[wg]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_half[wg]);
           }
         } else if constexpr (QUAD) {
           const int q0 = (warp & 3) * 32;  // this warp's quarter of the keys
@@ -1188,14 +1182,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tmem_st32(s_tm + 32, pk);
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&p_half[wg]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_half[wg]);
           probs(sa, pk);
           tmem_st32(s_tm, pk);
           l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
           tmem_st_wait();
         }
         tc_fence_before();
-        mbar_arrive(&p_full[wg]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[wg]);
       }
       if (!ok) break;
       // split: whether each stream had tiles
@@ -1226,7 +1222,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           a1 = fast_exp2(y1.x - mt);
           if constexpr (!QUAD) lt = y0.y * a0 + y1.y * a1;
         }
-        ok = wait_or_abort(o_full, n_q & 1, p.status, abort);
+        ok = warp_wait(o_full, n_q & 1, p.status, abort);
         if (!ok) break;
         ++n_q;
         tc_fence_after();
@@ -1277,7 +1273,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         if (d.n > 0) {
           tc_fence_before();
-          mbar_arrive(o_empty);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_empty);
         }
         float4* ms = merge_s + wg * (4 * SW / 4 * 32);
 #pragma unroll
@@ -1380,7 +1377,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (!QUAD && d.n > 0) {
         tc_fence_before();
-        mbar_arrive(o_empty);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_empty);
       }
       if (valid && (PAIR || warp == 0 || (!QUAD && wg == 0))) {
         if (d.parts > 1)

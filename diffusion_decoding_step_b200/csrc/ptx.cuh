@@ -436,6 +436,22 @@ DLLM_DEV void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
                : "memory");
 }
 
+// ---------------------------------------------------------------- uniform code
+// tcgen05 and TMA instructions take their operands from uniform registers.  The
+// compiler knows a value to be uniform if it comes from a shuffle of one lane or a
+// vote, and code to run in one lane if elect.sync chose it; otherwise it wraps
+// every such instruction in a loop over the lanes.
+DLLM_DEV int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+DLLM_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- misc
 DLLM_DEV float bf16_to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 
