@@ -288,6 +288,10 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //   warp 9      issues S = Q K^T and O += P V on tcgen05.  (One warp for each stream
 //               let the streams' products interleave and their softmaxes run at the
 //               same time: 187 us instead of 161 for the 32 samples.)
+//   warp 11     is the watchdog: the waits of the others are unbounded until it finds
+//               that nothing was multiplied for two seconds, reports that and lets
+//               them go.  (A clock in every wait made the code a tenth longer, and a
+//               launch pays for its code: it is fetched anew.)
 //   warps 0-3 and 4-7   softmax of two streams with their own S, P and O in
 //               TMEM, so that the products of one run during the softmax of the
 //               other.  A thread owns a query row; P overwrites S in TMEM as the
@@ -400,21 +404,11 @@ DLLM_DEV void trade_units(uint4 (&u)[N], int lane) {
   }
 }
 
-// A whole warp waits; false when it or another role gave up, which sets the flag.
-DLLM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+// A whole warp waits; false when the watchdog gave up.
+DLLM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
   bool ok = true;
-  unsigned long long t0 = 0;
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-    if ((i & 63u) != 0u) continue;
+  while (!mbar_try_wait(bar, parity)) {
     if (*abort) {
-      ok = false;
-      break;
-    }
-    const unsigned long long now = global_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) {
-      *abort = 1;
-      if (status) atomicOr(status, kErrTimeout);
       ok = false;
       break;
     }
@@ -480,8 +474,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* q_empty = q_full + 1;
   uint64_t* o_full = q_empty + 1;
   uint64_t* o_empty = o_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_empty + 1);
+  uint64_t* done = o_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* progress = abort + 1;
 
   const int t = threadIdx.x, warp = uniform(t >> 5), lane = t & 31;
   const int tile_rows = p.rows_per_tile * C::kQ;
@@ -508,7 +504,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     mbar_init(q_empty, 1);
     mbar_init(o_full, 1);
     mbar_init(o_empty, 8);
+    mbar_init(done, 11);
     *abort = 0;
+    *progress = 0;
     fence_barrier_init();
     prefetch_tmap(&qmap);
     prefetch_tmap(&kmap);
@@ -520,53 +518,65 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // ---- the line: row starts and groups (made non-decreasing, whatever they
   // hold, so that all CTAs agree on disjoint items), then a prefix sum
   const int n_seqs = p.bt.n_seqs;
-  constexpr int kPer = (kMaxSeqs + kAttnThreads - 1) / kAttnThreads;
-  const int per = (n_seqs + kAttnThreads - 1) / kAttnThreads;
   {
-    int kt[kPer], raw[kPer][4];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = t * per + j;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        raw[j][k] = j < per && i < n_seqs ? p.segs[4 * (size_t)i + k] : 0;
+    int4 raw = make_int4(0, 0, 0, 0);  // segments of sequence t
+    if (t < n_seqs) {
+      const int* g = p.segs + 4 * t;
+      raw = make_int4(g[0], g[1], g[2], g[3]);
     }
+#pragma unroll 1
     for (int i = t; i <= n_seqs; i += kAttnThreads)
       rs[i] = min(max(p.bt.row_start[i], 0), p.bt.n_rows);
     if constexpr (GROUPS) {
+#pragma unroll 1
       for (int i = t; i <= p.n_groups; i += kAttnThreads) {
         const int first = p.gseq[i];
         if (i < p.n_groups) pk[i] = prefix_keys(p, i);
         gs[i] = min(max(first, 0), n_seqs);
       }
     }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      kt[j] = seg_tiles(make_segs(p, raw[j][0], raw[j][1], raw[j][2], raw[j][3]));
     __syncthreads();
     bool bad = false;
+#pragma unroll 1
     for (int i = t; i < n_seqs; i += kAttnThreads) bad |= rs[i + 1] < rs[i];
-    if constexpr (GROUPS)
+    if constexpr (GROUPS) {
+#pragma unroll 1
       for (int i = t; i < p.n_groups; i += kAttnThreads) bad |= gs[i + 1] < gs[i];
+    }
     if (__syncthreads_or(bad)) {
       if (t == 0) {
+#pragma unroll 1
         for (int i = 0; i < n_seqs; ++i) rs[i + 1] = max(rs[i + 1], rs[i]);
-        if constexpr (GROUPS)
+        if constexpr (GROUPS) {
+#pragma unroll 1
           for (int i = 0; i < p.n_groups; ++i) gs[i + 1] = max(gs[i + 1], gs[i]);
+        }
       }
       __syncthreads();
     }
-    int* scratch = reinterpret_cast<int*>(x_s);
     int* opfx = reinterpret_cast<int*>(k_s);  // own key tiles of earlier sequences
-    int gr[kPer];  // the group of each sequence, or -1
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) gr[j] = -1;
-    if constexpr (GROUPS) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = t * per + j;
-        if (j >= per || i >= n_seqs) continue;
+    // v[1 .. n_seqs] becomes its prefix sum, v[0] zero; each thread has a run of it
+    const int per = (n_seqs + kAttnThreads - 1) / kAttnThreads;
+    auto prefix_sum = [&](int* v, int* scratch) {
+      __syncthreads();
+      const int i0 = min(t * per, n_seqs), i1 = min(i0 + per, n_seqs);
+      int sum = 0;
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i) sum += v[i + 1];
+      int before = block_before(sum, scratch, warp, lane);
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i) v[i + 1] = before += v[i + 1];
+      if (t == 0) v[0] = 0;
+    };
+    int* scratch = reinterpret_cast<int*>(x_s);
+#pragma unroll 1
+    for (int i = t; i < n_seqs; i += kAttnThreads) {
+      const int kt = seg_tiles(i == t ? make_segs(p, raw.x, raw.y, raw.z, raw.w) : seq_segs(p, i));
+      const int rows = rs[i + 1] - rs[i];
+      int g = -1;
+      if constexpr (GROUPS) {
         int lo = 0, hi = p.n_groups;  // the last group that starts at or before i
+#pragma unroll 1
         while (hi - lo > 1) {
           const int mid = (lo + hi) / 2;
           if (gs[mid] <= i)
@@ -574,60 +584,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           else
             hi = mid;
         }
-        if (gs[lo] <= i && i < gs[lo + 1] && pk[lo] > 0) gr[j] = lo;
-        gid[i] = (short)gr[j];
+        if (gs[lo] <= i && i < gs[lo + 1] && pk[lo] > 0) g = lo;
+        gid[i] = (short)g;
+        opfx[i + 1] = rows > 0 ? kt * (rows / tile_rows + 1) : 0;
       }
-      int own[kPer], sum = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = t * per + j;
-        own[j] = 0;
-        if (j < per && i < n_seqs && rs[i + 1] > rs[i])
-          own[j] = kt[j] * ((rs[i + 1] - rs[i]) / tile_rows + 1);
-        sum += own[j];
-      }
-      int before = block_before(sum, scratch + 16, warp, lane);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = t * per + j;
-        if (j < per && i < n_seqs) {
-          opfx[i] = before;
-          before += own[j];
-          if (i == n_seqs - 1) opfx[n_seqs] = before;
-        }
-      }
+      upfx[i + 1] =
+          g < 0 ? (rows + tile_rows - 1) / tile_rows * p.kv.Hkv * (max(kt, 1) + kTileCost) : 0;
+    }
+    if constexpr (GROUPS) {
+      prefix_sum(opfx, scratch + 16);
       __syncthreads();
-    }
-    int units[kPer], sum = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = t * per + j;
-      units[j] = 0;
-      if (j < per && i < n_seqs) {
-        const int g = gr[j];
-        if (g < 0) {
-          const int nt = (rs[i + 1] - rs[i] + tile_rows - 1) / tile_rows;
-          units[j] = nt * p.kv.Hkv * (max(kt[j], 1) + kTileCost);
-        } else if (GROUPS && i == gs[g]) {
-          const int nt = (rs[gs[g + 1]] - rs[i] + tile_rows - 1) / tile_rows;
-          const int own = opfx[gs[g + 1]] - opfx[i];
-          if (nt > 0)
-            units[j] = nt * p.kv.Hkv *
-                       (key_tiles(0, pk[g]) + (own + nt - 1) / nt + kTileCost);
-        }
-      }
-      sum += units[j];
-    }
-    int before = block_before(sum, scratch, warp, lane);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = t * per + j;
-      if (j < per && i < n_seqs) {
-        upfx[i] = before;
-        before += units[j];
-        if (i == n_seqs - 1) upfx[n_seqs] = before;
+#pragma unroll 1
+      for (int g = t; g < p.n_groups; g += kAttnThreads) {
+        const int i = gs[g], e = gs[g + 1];
+        const int nt = (rs[e] - rs[i] + tile_rows - 1) / tile_rows;
+        if (e > i && nt > 0 && pk[g] > 0)
+          upfx[i + 1] = nt * p.kv.Hkv *
+                        (key_tiles(0, pk[g]) + (opfx[e] - opfx[i] + nt - 1) / nt + kTileCost);
       }
     }
+    prefix_sum(upfx, scratch);
+    if constexpr (GROUPS) fence_proxy_async_smem();  // opfx was where K tiles will land
   }
   tc_fence_before();
   __syncthreads();
@@ -757,7 +734,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int qi = n_piece % kQueue;
       if (k_side) {
         ok = n_piece < kQueue ||
-             warp_wait(&d_empty[qi], (n_piece / kQueue - 1) & 1, p.status, abort);
+             warp_wait(&d_empty[qi], (n_piece / kQueue - 1) & 1, abort);
         if (ok && lane == 0) {
           Piece d{r0, nrows, kvh, n, 1, 2 * cta + (first_piece ? 0 : 1)};
           if (x0 > start + kTileCost || x1 < end) {
@@ -775,7 +752,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
       // ---- its loads
       if (k_side) {
-        ok = n_q == 0 || warp_wait(q_empty, (n_q - 1) & 1, p.status, abort);
+        ok = n_q == 0 || warp_wait(q_empty, (n_q - 1) & 1, abort);
         const int q_row = uniform(r0), q_head = uniform(kvh) * p.G;
         if (ok && elect_one()) {
           constexpr int kCopies = QUAD ? 4 : C::kQ;
@@ -844,7 +821,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int ti = n_tile + j;
         const int round = k_side ? ti / STK : ti / STV;
         const int st = uniform(k_side ? ti % STK : ti % STV);
-        ok = round == 0 || warp_wait(&empty[st], (round - 1) & 1, p.status, abort);
+        ok = round == 0 || warp_wait(&empty[st], (round - 1) & 1, abort);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTile);
         const int slot = uniform(page_keys == kKeyTile ? c.kb & slot_mask : 0);
@@ -871,7 +848,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (k_side) {
       const int qi = n_piece % kQueue;
       ok = ok && (n_piece < kQueue ||
-                  warp_wait(&d_empty[qi], (n_piece / kQueue - 1) & 1, p.status, abort));
+                  warp_wait(&d_empty[qi], (n_piece / kQueue - 1) & 1, abort));
       if (lane == 0) {
         if (ok) {
           queue[qi].n = -1;
@@ -893,7 +870,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bool ok = true;
       while (ok) {
         const int qi = n_piece % kQueue;
-        ok = warp_wait(&d_full[qi], (n_piece / kQueue) & 1, p.status, abort);
+        ok = warp_wait(&d_full[qi], (n_piece / kQueue) & 1, abort);
         if (!ok) break;
         const int n = uniform(queue[qi].n);
         const bool two = uniform(queue[qi].nrows) > p.rows_per_tile;  // rows in both halves
@@ -903,11 +880,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (n == 0) continue;
         auto wait_k = [&](int j) {
           const int ti = n_tile + j;
-          return warp_wait(&k_full[ti % STK], (ti / STK) & 1, p.status, abort);
+          return warp_wait(&k_full[ti % STK], (ti / STK) & 1, abort);
         };
         auto wait_v = [&](int j) {
           const int ti = n_tile + j;
-          return warp_wait(&v_full[ti % STV], (ti / STV) & 1, p.status, abort);
+          return warp_wait(&v_full[ti % STV], (ti / STV) & 1, abort);
         };
         // S of key tile j in stream x; after the last use K (and Q) are free
         auto s_mma = [&](int x, int j, bool last) {
@@ -943,14 +920,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           };
           const uint32_t parity = n_p[x]++ & 1;
           if constexpr (!QUAD) {
-            if (!warp_wait(&p_half[x], parity, p.status, abort)) return false;
+            if (!warp_wait(&p_half[x], parity, abort)) return false;
             tc_fence_after();
             if (elect_one()) steps(kSteps / 2, accumulate);
             __syncwarp();
           }
-          if (!warp_wait(&p_full[x], parity, p.status, abort)) return false;
+          if (!warp_wait(&p_full[x], parity, abort)) return false;
           tc_fence_after();
           if (elect_one()) {
+            *progress = n_tile + j + 1;
             if constexpr (QUAD) steps(kSteps / 2, accumulate);
             steps(0, true);
             if (last) umma_commit(&v_empty[st]);
@@ -958,38 +936,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           __syncwarp();
           return true;
         };
-        ok = warp_wait(q_full, n_q & 1, p.status, abort) && wait_k(0);
+        ok = warp_wait(q_full, n_q & 1, abort);
         if (!ok) break;
-        tc_fence_after();
-        if constexpr (PAIR) {
-          s_mma(0, 0, !two);
-          if (two) s_mma(1, 0, true);
-          ok = n_q == 0 || warp_wait(o_empty, (n_q - 1) & 1, p.status, abort);
-          for (int j = 0; ok && j < n; ++j) {
-            const bool more = j + 1 < n;
-            ok = wait_v(j) && pv_mma(0, j, j > 0, !two) && (!more || wait_k(j + 1));
-            if (!ok) break;
+        // Each turn takes P of a stream, multiplies it, and issues the stream's next S.
+        // Pairs: the streams by turns, each with every tile; else a tile a turn, the
+        // streams in turn from the one that the last piece did not end with.
+        const int b = PAIR ? 0 : n_tile & 1, streams = PAIR && !two ? 1 : 2;
+        const int turns = PAIR && two ? 2 * n : n;
+#pragma unroll 1
+        for (int i = -streams; ok && i < turns; ++i) {
+          const int x = streams == 1 ? 0 : (b + i) & 1;
+          const int j = PAIR && two ? i >> 1 : i, j_s = PAIR ? j + 1 : i + 2;
+          const bool last = !PAIR || x == streams - 1;  // the tile's last use
+          if (i == 0) ok = n_q == 0 || warp_wait(o_empty, (n_q - 1) & 1, abort);
+          if (ok && i >= 0)
+            ok = (PAIR && x == 1 || wait_v(j)) && pv_mma(x, j, PAIR ? j > 0 : j > 1, last);
+          if (ok && j_s < n) {
+            ok = (PAIR && x == 1) || wait_k(j_s);
             tc_fence_after();
-            if (more) s_mma(0, j + 1, !two);
-            if (two) {
-              ok = pv_mma(1, j, j > 0, true);
-              if (ok && more) s_mma(1, j + 1, true);
-            }
-          }
-        } else {
-          const int b = n_tile & 1;  // the streams take tiles in turn
-          s_mma(b, 0, true);
-          if (n > 1 && (ok = wait_k(1))) {
-            tc_fence_after();
-            s_mma(b ^ 1, 1, true);
-          }
-          ok = ok && (n_q == 0 || warp_wait(o_empty, (n_q - 1) & 1, p.status, abort));
-          for (int j = 0; ok && j < n; ++j) {
-            ok = wait_v(j) && pv_mma((b + j) & 1, j, j > 1, true);
-            if (ok && j + 2 < n && (ok = wait_k(j + 2))) {
-              tc_fence_after();
-              s_mma((b + j) & 1, j + 2, true);
-            }
+            if (ok) s_mma(x, j_s, last);
           }
         }
         if (ok && elect_one()) umma_commit(o_full);
@@ -1012,7 +977,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bool ok = true;
     while (ok) {
       const int qi = n_piece % kQueue;
-      ok = warp_wait(&d_full[qi], (n_piece / kQueue) & 1, p.status, abort);
+      ok = warp_wait(&d_full[qi], (n_piece / kQueue) & 1, abort);
       if (!ok) break;
       const Piece d{uniform(queue[qi].r0), uniform(queue[qi].nrows), uniform(queue[qi].kvh),
                     uniform(queue[qi].n), uniform(queue[qi].parts), uniform(queue[qi].slot)};
@@ -1048,7 +1013,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int j0 = PAIR ? 0 : (wg ^ n_tile) & 1;  // split: the streams take tiles in turn
       for (int j = j0; stream && j < d.n; j += PAIR ? 1 : 2) {
         const int ti = n_tile + j;
-        ok = warp_wait(&t_full[ti % kTileQueue], (ti / kTileQueue) & 1, p.status, abort);
+        ok = warp_wait(&t_full[ti % kTileQueue], (ti / kTileQueue) & 1, abort);
         if (!ok) break;
         const int4 tl = tiles_s[ti % kTileQueue];  // base, lo, hi, rows
         const bool own = tl.w >> 18;
@@ -1058,7 +1023,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool sees = __any_sync(0xffffffffu, end_k > first_k);
         const bool masked =
             __any_sync(0xffffffffu, valid && (first_k > 0 || end_k < kKeyTile));
-        ok = warp_wait(&s_full[wg], s_cnt & 1, p.status, abort);
+        ok = warp_wait(&s_full[wg], s_cnt & 1, abort);
         if (!ok) break;
         ++s_cnt;
         tc_fence_after();
@@ -1069,7 +1034,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (tl.y > tl.x || tl.z < tl.x + kKeyTile) {
           const int key = tl.x + row;
           const int pg = key & ~(page_keys - 1);
-          ok = warp_wait(&v_full[ti % STV], (ti / STV) & 1, p.status, abort);
+          ok = warp_wait(&v_full[ti % STV], (ti / STV) & 1, abort);
           if (!ok) break;
           if ((key < tl.y || key >= tl.z) && pg < tl.z && pg + page_keys > tl.y) {
             uint4* v = reinterpret_cast<uint4*>(v_s + (ti % STV) * C::kTile + row * C::kRowBytes);
@@ -1222,7 +1187,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           a1 = fast_exp2(y1.x - mt);
           if constexpr (!QUAD) lt = y0.y * a0 + y1.y * a1;
         }
-        ok = warp_wait(o_full, n_q & 1, p.status, abort);
+        ok = warp_wait(o_full, n_q & 1, abort);
         if (!ok) break;
         ++n_q;
         tc_fence_after();
@@ -1248,42 +1213,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // four are added through shared memory, SW columns at a time, of which
         // each warp finishes SW / 4
         constexpr int SW = kC, kOwn = SW / 4;
-        float v[kCols / SW][SW];
-#pragma unroll
+        float4* ms = merge_s + wg * (4 * SW / 4 * 32);
+#pragma unroll 1
         for (int c = 0; c < kCols / SW; ++c) {
+          float v[SW];
 #pragma unroll
-          for (int i = 0; i < SW; ++i) v[c][i] = 0.f;
+          for (int i = 0; i < SW; ++i) v[i] = 0.f;
           if (active) {
-            float w[SW];
-            const uint32_t at = o_tm + c0 + c * SW;
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < 2; ++x) {
               if (!(x ? some1 : some0)) continue;
+              float w[SW];
+              const uint32_t at = o_tm + c0 + c * SW + x * 128;
               if constexpr (SW == 32) {
-                tmem_ld32(at + x * 128, w);
+                tmem_ld32(at, w);
                 tmem_ld_wait32(w);
               } else {
-                tmem_ld16(at + x * 128, reinterpret_cast<float(&)[16]>(w));
+                tmem_ld16(at, reinterpret_cast<float(&)[16]>(w));
                 tmem_ld_wait16(w);
               }
+              const float a = x ? a1 : a0;
 #pragma unroll
-              for (int i = 0; i < SW; ++i) v[c][i] = fmaf(w[i], x ? a1 : a0, v[c][i]);
+              for (int i = 0; i < SW; ++i) v[i] = fmaf(w[i], a, v[i]);
             }
           }
-        }
-        if (d.n > 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(o_empty);
-        }
-        float4* ms = merge_s + wg * (4 * SW / 4 * 32);
-#pragma unroll
-        for (int c = 0; c < kCols / SW; ++c) {
+          if (c == kCols / SW - 1 && d.n > 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_empty);
+          }
           named_bar_sync(2 + wg, 128);  // the buffer is free
 #pragma unroll
           for (int k = 0; k < SW / 4; ++k)
             ms[((warp & 3) * (SW / 4) + k) * 32 + lane] =
-                make_float4(v[c][4 * k], v[c][4 * k + 1], v[c][4 * k + 2], v[c][4 * k + 3]);
+                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           named_bar_sync(2 + wg, 128);
           float o[kOwn];
 #pragma unroll
@@ -1389,9 +1352,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     }
   }
-  if (*abort) {  // copies and products in flight end before the block goes
-    const unsigned long long t0 = global_ns();
-    while (global_ns() - t0 < 100000ull) __nanosleep(1000);
+  if (warp == 11) {
+    // ================================================================ watchdog
+    int seen = 0;
+    unsigned long long t0 = global_ns();
+    while (!mbar_try_wait_sleep(done, 0, 100000u)) {
+      const int now = *progress;
+      if (now != seen) {
+        seen = now;
+        t0 = global_ns();
+      } else if (!*abort && global_ns() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        if (lane == 0 && p.status != nullptr) atomicOr(p.status, kErrTimeout);
+      }
+    }
+  } else {
+    if (*abort) {  // copies and products in flight end before the block goes
+      const unsigned long long t0 = global_ns();
+      while (global_ns() - t0 < 100000ull) __nanosleep(1000);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(done);
   }
   __syncwarp();
   tc_fence_before();
