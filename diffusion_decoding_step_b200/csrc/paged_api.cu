@@ -266,6 +266,8 @@ dllm_status dllm_paged_workspace_size(const dllm_kv_pages* kv, int32_t n_q_heads
 dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream stream) {
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return DLLM_ERR_INVALID;
   if (ws_bytes < kWsParts) return DLLM_ERR_WORKSPACE;
+  const dllm_status e = prepare_device();  // so that the first attention may be a captured one
+  if (e != DLLM_OK) return e;
   return cudaMemsetAsync(ws, 0, 256, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? DLLM_OK
              : DLLM_ERR_CUDA;

@@ -15,8 +15,9 @@ from . import abi
 
 _TYPES = {torch.bfloat16: abi.DLLM_KV_BF16, torch.float16: abi.DLLM_KV_F16}
 
-
-_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index; current_stream() costs 2 us
+# the current stream of a device index, and the current device: the public calls
+# (current_stream, current_device) take 2.2 and 0.2 us of a call's 11
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _ints(t: torch.Tensor, what: str, shape: tuple, index: int) -> int:
@@ -80,7 +81,7 @@ class PagedKV:
 
     # ------------------------------------------------------------------ arguments
     def _call(self, what: str, fn, *args) -> None:
-        if torch.cuda.current_device() == self._index:
+        if _current_device() == self._index:
             status = fn(*args, _raw_stream(self._index))
         else:
             with torch.cuda.device(self.device):

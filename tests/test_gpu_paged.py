@@ -322,6 +322,14 @@ SHARED = [  # dtype, D, Hq, Hkv, page, layout, rows, own segments, (first sequen
     (HF, 32, 4, 4, 8, "padded", [8, 8, 8, 8], whole(8, 0, 8, 130), ([0, 2, 4], [0, 257])),
     (BF, 128, 7, 1, 128, "heads", [1, 1, 1, 1, 1], whole(0, 0, 0, 0, 0), ([0, 2, 4], [9000, 3])),
     (HF, 128, 14, 2, 16, "heads", [40] * 9, whole(*range(40, 400, 40)), ([0, 9], [1000])),
+    # one query tile spans more sequences than a warp has lanes, some of them without rows
+    (BF, 64, 2, 2, 16, "heads", [1 if i % 4 else 0 for i in range(200)],
+     whole(*[(i * 7) % 41 for i in range(200)]), ([3, 190], [300])),
+    (HF, 32, 3, 3, 8, "slots", [2] * 150, whole(*[i % 19 for i in range(150)]), ([0, 150], [129])),
+    # every kind of sequence and group in one batch
+    (BF, 128, 8, 2, 32, "heads", [1, 70, 0, 33, 1, 1, 200, 5], whole(300, 70, 50, 0, 1, 129, 700, 5),
+     ([1, 2, 2, 5, 7], [128, 90, 1, 640])),
+    (HF, 64, 64, 1, 64, "padded", [1, 3, 2], whole(9, 3, 200), ([0, 2, 3], [64, 65])),
 ]
 
 
@@ -330,9 +338,52 @@ def test_shared_prefix(case):
     run_attn(*case[:8], groups=case[8])
 
 
+def test_many_sequences_and_groups():
+    """More sequences than the threads that plan the work, in hundreds of groups."""
+    n = 1000
+    run_attn(BF, 32, 2, 1, 8, "heads", [(i * 5) % 3 for i in range(n)], whole(*[(i * 13) % 30 for i in range(n)]))
+    run_attn(HF, 32, 2, 1, 8, "slots", [1 if i % 9 else 0 for i in range(n)], whole(*[i % 12 for i in range(n)]),
+             groups=([min(3 * i + i % 2, n) for i in range(331)], [(i * 11) % 50 for i in range(330)]))
+
+
+def test_first_call_may_be_captured():
+    """In a process of its own: the first attention of all is a captured one."""
+    import subprocess
+    import sys
+
+    from tests.conftest import ROOT
+    code = ("import torch, sys; sys.path.insert(0, %r)\n"
+            "from tests.test_gpu_paged import *\nfrom tests.test_gpu_paged import _gen\n"
+            "g = _gen(1); pool = make_pool(g, 4, 2, 16, 64, BF, 'heads'); kv = make_kv(pool, 4, 3)\n"
+            "q = torch.randn(3, 4, 64, generator=g).to(BF).to(DEV); out = torch.zeros_like(q)\n"
+            "a = (q, ints([0, 3]), ints([[2, 0]]), ints(whole(20)))\n"
+            "gr = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(gr):\n    kv.attn(*a, out=out)\n"
+            "gr.replay(); torch.cuda.synchronize()\n"
+            "check_rows(out, R.attention(host(pool), q.cpu(), [0, 3], a[2].cpu(), whole(20)))\n" % ROOT)
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_calls_follow_their_pages_device_stream():
+    """Back-to-back calls on a side stream see what was queued there before them."""
+    g = _gen(31)
+    pool = make_pool(g, 8, 2, 16, 64, BF, "heads")
+    kv = make_kv(pool, 4, 4)
+    x = torch.randn(4, 8, 64, generator=g).to(BF)
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        d = x.pin_memory().to(DEV, non_blocking=True)
+        q = kv.append(d[:, 4:6], d[:, 6:], ints([0, 4]), ints([[5, 1]]), ints([14]), q=d[:, :4], rope_theta=1e4)
+        out = kv.attn(q, ints([0, 4]), ints([[5, 1]]), ints(whole(18)))
+        assert kv.device_status() == 0      # waits for the stream
+    ref = R.attention(host(pool), q.cpu(), [0, 4], torch.tensor([[5, 1]], dtype=torch.int32), whole(18))
+    check_rows(out, ref)
+
+
 def test_shared_prefix_row_limits_count_own_positions():
-    c = SHARED[1]
-    run_attn(*c[:8], groups=c[8], limit=lambda s, j: j)
+    for c in (SHARED[1], SHARED[5], SHARED[8]):
+        run_attn(*c[:8], groups=c[8], limit=lambda s, j: j)
 
 
 def test_bad_pages_read_as_zeros():
