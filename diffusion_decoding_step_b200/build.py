@@ -1,4 +1,5 @@
-"""Build libdllm.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc."""
+"""Build libdllm.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and the
+torch binding of its paged cache calls with the host compiler."""
 from __future__ import annotations
 
 import os
@@ -13,6 +14,8 @@ LIB = os.path.join(HERE, "libdllm.so")
 # range-checked in the kernels (an error bit instead of an access).
 LIB_DEBUG = os.path.join(HERE, "libdllm_debug.so")
 SOURCES = ["api.cu", "gemm.cu", "attn.cu", "small.cu", "stack.cu", "paged_api.cu", "paged.cu"]
+# Python module that takes torch tensors (csrc/paged_torch.cpp)
+BINDING = os.path.join(HERE, "_paged_torch.so")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr"]
 
@@ -28,15 +31,42 @@ def stale(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
     deps.append(os.path.join(HERE, "..", "include", "dllm.h"))
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the torch binding of the paged cache calls into _paged_torch.so."""
+    src = os.path.join(CSRC, "paged_torch.cpp")
+    deps = [src, os.path.join(HERE, "..", "include", "dllm.h")]
+    if not force and os.path.exists(BINDING) \
+            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + ".tmp"
+    subprocess.run(
+        [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(root, "include"),
+         "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+         "-I" + os.path.join(cuda, "include"), src, "-o", tmp,
+         "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+         "-lc10_cuda"], check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile every CUDA source into libdllm.so next to this file (with
-    debug=True: libdllm_debug.so, the DLLM_DEBUG build)."""
+    debug=True: libdllm_debug.so, the DLLM_DEBUG build), and the torch binding."""
     lib = LIB_DEBUG if debug else LIB
+    if not debug:
+        build_binding(force)
     if not force and not stale(lib):
         return lib
     cmd = [nvcc(), *FLAGS]

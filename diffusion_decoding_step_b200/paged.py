@@ -2,7 +2,8 @@
 
 PyTorch only allocates memory and provides the stream; the arithmetic runs in
 libdllm.so (``dllm_paged_append``, ``dllm_paged_attn``,
-``dllm_shared_prefix_attn``; include/dllm.h states what they compute).
+``dllm_shared_prefix_attn``; include/dllm.h states what they compute).  The
+tensors are checked and passed on by the compiled module ``_paged_torch``.
 """
 from __future__ import annotations
 
@@ -15,18 +16,15 @@ from . import abi
 
 _TYPES = {torch.bfloat16: abi.DLLM_KV_BF16, torch.float16: abi.DLLM_KV_F16}
 
-# the current stream of a device index, and the current device: the public calls
-# (current_stream, current_device) take 2.2 and 0.2 us of a call's 11
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
-
-def _ints(t: torch.Tensor, what: str, shape: tuple, index: int) -> int:
-    """Address of a contiguous int32 tensor of the given shape on GPU `index`."""
-    if t.dtype is torch.int32 and t.shape == shape and t.get_device() == index \
-            and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{what}: a contiguous int32 tensor of shape {list(shape)} on cuda:{index} is "
-                     f"needed, got {t.dtype} {list(t.shape)} on {t.device}")
+def _binding():
+    """The compiled binding; fails loudly if it has not been built."""
+    try:
+        from . import _paged_torch
+    except ImportError as e:
+        raise abi.DllmError(f"torch binding not built or not loadable ({e}); run "
+                            "diffusion_decoding_step_b200/build.py") from e
+    return _paged_torch
 
 
 class PagedKV:
@@ -57,54 +55,26 @@ class PagedKV:
             raise ValueError("the D elements of a head have to be contiguous")
         self.k_pages, self.v_pages = k_pages, v_pages
         self.device, self.dtype = k_pages.device, k_pages.dtype
-        self._index = k_pages.get_device()
         n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_pages.shape
         self.n_q_heads, self.max_rows, self.max_groups = n_q_heads, max_rows, max_groups
-        lib = abi.lib()
-        self._append, self._attn = lib.dllm_paged_append, lib.dllm_paged_attn
-        self._shared, self._status = lib.dllm_shared_prefix_attn, lib.dllm_device_status
-        self._kv = abi.dllm_kv_pages(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.stride(0),
-                                     k_pages.stride(1), k_pages.stride(2), n_pages,
-                                     self.page_size, self.n_kv_heads, self.head_dim,
-                                     _TYPES[self.dtype])
-        self._kv_p = C.byref(self._kv)
+        binding, lib = _binding(), abi.lib()
+        kv = abi.dllm_kv_pages(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.stride(0),
+                               k_pages.stride(1), k_pages.stride(2), n_pages, self.page_size,
+                               self.n_kv_heads, self.head_dim, _TYPES[self.dtype])
         n = C.c_size_t(0)
-        abi.check(abi.dllm_paged_workspace_size(self._kv_p, n_q_heads, max_rows, C.byref(n)),
+        abi.check(abi.dllm_paged_workspace_size(C.byref(kv), n_q_heads, max_rows, C.byref(n)),
                   "paged_workspace_size")
-        self.ws_bytes = int(n.value)
         with torch.cuda.device(self.device):
-            self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
-            self._ws_p = self.ws.data_ptr()
-            abi.check(abi.dllm_paged_workspace_init(self._ws_p, self.ws_bytes,
-                                                    _raw_stream(self._index)),
+            self.ws = torch.empty(int(n.value), dtype=torch.uint8, device=self.device)
+            stream = torch.cuda.current_stream(self.device).cuda_stream
+            abi.check(abi.dllm_paged_workspace_init(self.ws.data_ptr(), n.value, stream),
                       "paged_workspace_init")
-
-    # ------------------------------------------------------------------ arguments
-    def _call(self, what: str, fn, *args) -> None:
-        if _current_device() == self._index:
-            status = fn(*args, _raw_stream(self._index))
-        else:
-            with torch.cuda.device(self.device):
-                status = fn(*args, _raw_stream(self._index))
-        if status != abi.DLLM_OK:
-            abi.check(status, what)
-
-    def _rows(self, t: torch.Tensor, what: str, n_rows: int, heads: int):
-        if t.dtype is self.dtype and t.shape == (n_rows, heads, self.head_dim) \
-                and t.get_device() == self._index:
-            row, head, one = t.stride()
-            if one == 1:
-                return C.byref(abi.dllm_rows(t.data_ptr(), row, head))
-        raise ValueError(f"{what}: a {self.dtype} tensor [{n_rows}][{heads}][{self.head_dim}] on "
-                         f"{self.device} with contiguous heads is needed, got {t.dtype} "
-                         f"{list(t.shape)}, strides {t.stride()}, on {t.device}")
-
-    def _batch(self, n_rows: int, row_start: torch.Tensor, page_table: torch.Tensor):
-        n = row_start.numel() - 1
-        width = page_table.shape[-1]
-        return n, C.byref(abi.dllm_paged_batch(
-            n, n_rows, width, width, _ints(row_start, "row_start", (n + 1,), self._index),
-            _ints(page_table, "page_table", (n, width), self._index)))
+        fns = (C.cast(f, C.c_void_p).value for f in (lib.dllm_paged_append, lib.dllm_paged_attn,
+                                                     lib.dllm_shared_prefix_attn))
+        self._append, self._attn = binding.append, binding.attn
+        self._h = binding.create(C.addressof(kv), n_q_heads, max_rows, max_groups,
+                                 self.device.index, int(self.dtype is torch.float16),
+                                 self.ws.data_ptr(), n.value, *fns)
 
     # ------------------------------------------------------------------ calls
     def append(self, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
@@ -116,44 +86,22 @@ class PagedKV:
 
         Rows [row_start[s], row_start[s+1]) go to positions pos[s].. of sequence s, rotated by
         position + rope_shift[s]; page_table [n_seqs][pages] lists each sequence's pages."""
-        rows, index = k.shape[0], self._index
-        n, bt = self._batch(rows, row_start, page_table)
-        heads, qp, qo = 0, None, None
         if q is not None:
             if q_out is None:
                 q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            heads = self.n_q_heads
-            qp = self._rows(q, "q", rows, heads)
-            qo = self._rows(q_out, "q_out", rows, heads)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        self._call("paged_append", self._append, self._kv_p, bt, heads, qp,
-                   self._rows(k, "k", rows, self.n_kv_heads),
-                   self._rows(v, "v", rows, self.n_kv_heads), qo, _ints(pos, "pos", (n,), index),
-                   None if rope_shift is None else _ints(rope_shift, "rope_shift", (n,), index),
-                   rope_theta, self._ws_p)
+        status = self._append(self._h, k, v, row_start, page_table, pos, q, q_out, rope_theta,
+                              rope_shift)
+        if status:
+            abi.check(status, "paged_append")
         return q_out
 
-    def _attn_args(self, q, row_start, page_table, segs, row_limit, out, lse):
-        rows = q.shape[0]
-        if rows > self.max_rows:
-            raise ValueError(f"{rows} rows: this PagedKV was made for {self.max_rows}")
-        n, bt = self._batch(rows, row_start, page_table)
-        if out is None:
-            out = torch.empty(rows, self.n_q_heads, self.head_dim, dtype=self.dtype,
-                              device=self.device)
-        lp = None
-        if lse is not None:
-            if lse.dtype is not torch.float32 or lse.shape != (rows, self.n_q_heads) \
-                    or lse.get_device() != self._index or not lse.is_contiguous():
-                raise ValueError(f"lse: a contiguous float32 tensor [{rows}][{self.n_q_heads}] on "
-                                 f"{self.device} is needed")
-            lp = lse.data_ptr()
-        return out, bt, (_ints(segs, "segs", (n, 2, 2), self._index),
-                         None if row_limit is None
-                         else _ints(row_limit, "row_limit", (rows,), self._index)), \
-            (self._rows(q, "q", rows, self.n_q_heads), self._rows(out, "out", rows, self.n_q_heads),
-             lp, self._ws_p, self.ws_bytes)
+    def _out(self, q):
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q: a tensor [rows][Hq][D] is needed")
+        return torch.empty(q.shape[0], self.n_q_heads, self.head_dim, dtype=self.dtype,
+                           device=self.device)
 
     def attn(self, q: torch.Tensor, row_start: torch.Tensor, page_table: torch.Tensor,
              segs: torch.Tensor, row_limit: Optional[torch.Tensor] = None, scale: float = 0.0,
@@ -165,8 +113,12 @@ class PagedKV:
         segs int32 [n_seqs][2][2]: (start, length) of the positions a sequence's rows see;
         row_limit int32 [rows]: a row sees only positions below it.  Rows of no sequence are
         left as they were (undefined in a fresh out)."""
-        out, bt, keys, rest = self._attn_args(q, row_start, page_table, segs, row_limit, out, lse)
-        self._call("paged_attn", self._attn, self._kv_p, bt, self.n_q_heads, *keys, scale, *rest)
+        if out is None:
+            out = self._out(q)
+        status = self._attn(self._h, q, row_start, page_table, segs, row_limit, scale, out, lse,
+                            None, None, None)
+        if status:
+            abi.check(status, "paged_attn")
         return out
 
     def shared_prefix_attn(self, q: torch.Tensor, row_start: torch.Tensor,
@@ -178,21 +130,21 @@ class PagedKV:
         """attn() for sequences that share prefixes: sequences [group_start[g],
         group_start[g+1]) also see the prefix_len[g] positions of the pages in
         prefix_table[g]."""
-        out, bt, keys, rest = self._attn_args(q, row_start, page_table, segs, row_limit, out, lse)
-        n, index = group_start.numel() - 1, self._index
-        if n < 1 or n > self.max_groups:
-            raise ValueError(f"{n} prefix groups: this PagedKV was made for 1 to {self.max_groups}")
-        width = prefix_table.shape[-1]
-        g = abi.dllm_prefix_groups(n, width, width,
-                                   _ints(group_start, "group_start", (n + 1,), index),
-                                   _ints(prefix_table, "prefix_table", (n, width), index),
-                                   _ints(prefix_len, "prefix_len", (n,), index))
-        self._call("shared_prefix_attn", self._shared, self._kv_p, bt, C.byref(g), self.n_q_heads,
-                   *keys, scale, *rest)
+        if group_start is None:
+            raise ValueError("group_start: a tensor is needed (attn() takes no groups)")
+        if out is None:
+            out = self._out(q)
+        status = self._attn(self._h, q, row_start, page_table, segs, row_limit, scale, out, lse,
+                            group_start, prefix_table, prefix_len)
+        if status:
+            abi.check(status, "shared_prefix_attn")
         return out
 
     def device_status(self) -> int:
         """The workspace's status word (waits for the current stream)."""
         code = C.c_int32(0)
-        self._call("device_status", self._status, self._ws_p, C.byref(code))
+        with torch.cuda.device(self.device):
+            stream = torch.cuda.current_stream(self.device).cuda_stream
+            abi.check(abi.dllm_device_status(self.ws.data_ptr(), C.byref(code), stream),
+                      "device_status")
         return int(code.value)

@@ -596,6 +596,11 @@ def test_arguments_are_checked():
         lambda: kv.attn(q, rs, tab, segs, lse=torch.zeros(3, 3, device=DEV)),
         lambda: kv.attn(q, rs, tab, segs, out=q[:2]),
         lambda: kv.shared_prefix_attn(q, rs, tab, segs, ints([0, 1, 1]), ints([[2], [3]]), ints([4, 4])),
+        lambda: kv.shared_prefix_attn(q, rs, tab, segs, None, None, None),
+        lambda: kv.shared_prefix_attn(q, rs, tab, segs, ints([0, 1]), ints([[2]]), None),
+        lambda: kv.attn(None, rs, tab, segs),
+        lambda: kv.attn(q, [0, 3], tab, segs),
+        lambda: kv.attn(q, rs, tab[0], segs),
         lambda: kv.append(k, k[:2], rs, tab, pos),
         lambda: kv.append(k, k, rs, tab, ints([0, 0])),
         lambda: kv.append(k, k, rs, tab, pos, q_out=q),
