@@ -311,7 +311,14 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //
 // A query tile that one CTA did alone is written out.  The parts of a cut tile
 // go to the workspace in fp32, and a second kernel merges them in the order of
-// the keys.
+// the keys.  Most cut tiles have two parts, the end of one CTA's share and the
+// start of the next one's, which is done long before: with 256-row tiles, whose
+// parts are large, a CTA that finds the other part of its tile announced takes it
+// from the workspace and writes the tile out, so that half the parts are never
+// written and the second kernel has little to do (prompt chunks 92 -> 86 us; with
+// the smaller tiles looking costs more than it saves, 32 tokens 57 -> 60).  Nothing waits for a part; where both CTAs miss the
+// other's, the second kernel does that tile as well.  Whoever adds two parts up
+// rounds in the same places, so results do not depend on who comes first.
 constexpr int kKeyTile = 128;
 constexpr int kAttnThreads = 384;
 constexpr int kMaxSeqs = 1024;
@@ -324,6 +331,7 @@ struct Piece {
   int r0, nrows, kvh, n;        // first row, rows, kv head, key tiles (-1: no more pieces)
   int parts;                    // parts of the query tile
   int slot;                     // partial slot: 2 * CTA, + 1 where it is not the CTA's first piece
+  int first, other;             // two parts: CTA of the first one; slot of the other one
 };
 
 template <int D, int MODE>
@@ -378,6 +386,14 @@ struct Shares {
                    : rem + (int)((unsigned)(u - big) / (unsigned)each);
   }
 };
+
+// Two parts by their weights, rounded in the same places wherever it is done.
+DLLM_DEV float two_parts(float x, float wx, float y, float wy) {
+  return __fmaf_rn(y, wy, __fmul_rn(x, wx));
+}
+DLLM_DEV float log_sum(float m, float l) {  // of a maximum in log2 units and a sum
+  return l > 0.f ? __fmaf_rn(0.6931471805599453f, m, logf(l)) : -INFINITY;
+}
 
 // Transpose of N units of 16 bytes among N neighbouring lanes (N = 2 or 4): after it
 // unit i of a lane is unit (lane % N) of the i-th lane of the group.
@@ -444,6 +460,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                       const __grid_constant__ PagedAttnParams p) {
   using C = PagedCfg<D, MODE>;
   constexpr bool PAIR = MODE == kPair, QUAD = MODE == kQuad;
+  constexpr bool kTakes = PAIR;  // whether a CTA may finish a tile of two parts
   constexpr int STK = C::kSTK, STV = C::kSTV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -478,6 +495,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* progress = abort + 1;
+  volatile int* other_s = progress + 1;  // [2]
 
   const int t = threadIdx.x, warp = uniform(t >> 5), lane = t & 31;
   const int tile_rows = p.rows_per_tile * C::kQ;
@@ -627,6 +645,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       u1 = sh.start(cta + 1);
     }
     int4 cut = make_int4(0, 0, 0, 0);
+    const int epoch = kTakes ? *p.epoch + 2 : 0;
     int i = 0, hi = n_seqs;  // the last sequence that starts at or before u
     while (hi - i > 1) {
       const int mid = (i + hi) / 2;
@@ -736,11 +755,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ok = n_piece < kQueue ||
              warp_wait(&d_empty[qi], (n_piece / kQueue - 1) & 1, abort);
         if (ok && lane == 0) {
-          Piece d{r0, nrows, kvh, n, 1, 2 * cta + (first_piece ? 0 : 1)};
+          Piece d{r0, nrows, kvh, n, 1, 2 * cta + (first_piece ? 0 : 1), cta, 0};
           if (x0 > start + kTileCost || x1 < end) {
-            d.parts = sh.owner(end - 1) - sh.owner(start + kTileCost) + 1;
-            if (x0 == start + kTileCost)
-              cut = make_int4(r0, nrows, kvh, d.parts | (d.slot & 1) << 16);  // (lane 0's)
+            d.first = sh.owner(start + kTileCost);
+            d.parts = sh.owner(end - 1) - d.first + 1;
+            d.other = d.first == cta ? 2 * (cta + 1) : 2 * d.first + (sh.start(d.first) < start);
+            if (d.first == cta)  // (lane 0's)
+              cut = make_int4(r0, nrows | kvh << 12, epoch, d.parts | (d.slot & 1) << 16);
           }
           queue[qi] = d;
           mbar_arrive(&d_full[qi]);
@@ -973,14 +994,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int row_in = qrow / p.G, hh = qrow - row_in * p.G;
     const int rr = row_in + (PAIR ? wg * p.rows_per_tile : 0);  // row within the query tile
     const int page_keys = min(kKeyTile, 1 << p.kv.page_shift);
-    int n_piece = 0, n_q = 0, s_cnt = 0, n_tile = 0;
+    int n_piece = 0, n_q = 0, s_cnt = 0, n_tile = 0, n_two = 0;
+    const int epoch = kTakes ? *p.epoch + 2 : 0;
     bool ok = true;
     while (ok) {
       const int qi = n_piece % kQueue;
       ok = warp_wait(&d_full[qi], (n_piece / kQueue) & 1, abort);
       if (!ok) break;
       const Piece d{uniform(queue[qi].r0), uniform(queue[qi].nrows), uniform(queue[qi].kvh),
-                    uniform(queue[qi].n), uniform(queue[qi].parts), uniform(queue[qi].slot)};
+                    uniform(queue[qi].n), uniform(queue[qi].parts), uniform(queue[qi].slot),
+                    uniform(queue[qi].first), uniform(queue[qi].other)};
       if (lane == 0) mbar_arrive(&d_empty[qi]);
       ++n_piece;
       if (d.n < 0) break;
@@ -1163,7 +1186,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const bool some0 = d.n > 1 || (d.n == 1 && (n_tile & 1) == 0);
       const bool some1 = d.n > 1 || (d.n == 1 && (n_tile & 1) == 1);
       n_tile += d.n;
-      // ---- the piece's result
+      // ---- the piece's result; of a tile of two parts, whether the other one is there
+      bool take = false;
+      if (kTakes && d.parts == 2) {
+        volatile int* there = other_s + (n_two++ & 1);
+        if (t == 0) *there = ld_acquire_gpu(p.ready + d.first) == epoch;
+        named_bar_sync(1, 256);
+        take = uniform(*there);
+      }
       float a0 = 1.f, a1 = 0.f, mt = m, lt = l;
       if (d.n > 0) {
         if constexpr (!PAIR) {  // (max, sum) of both streams; each takes half of the columns
@@ -1201,11 +1231,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int part_row = (PAIR ? wg * 128 : 0) + qrow;
       float4* part =
           reinterpret_cast<float4*>(p.part) + (size_t)d.slot * p.slot_rows * (D / 4) + part_row;
+      const float4* with = reinterpret_cast<const float4*>(p.part) +
+                           (size_t)d.other * p.slot_rows * (D / 4) + part_row;
+      const bool own_first = d.first == (int)blockIdx.x;
+      float w_own = 1.f, w_with = 0.f;  // weights of the two parts
+      if (kTakes && take && valid) {
+        const float2 y = __ldcg(&p.part_ml[(size_t)d.other * p.slot_rows + part_row]);
+        if (y.y > 0.f) {
+          const float both = fmaxf(mt, y.x);
+          w_own = fast_exp2(mt - both);
+          w_with = fast_exp2(y.x - both);
+          lt = own_first ? two_parts(lt, w_own, y.y, w_with) : two_parts(y.y, w_with, lt, w_own);
+          mt = both;
+        }
+      }
+      const bool whole = d.parts == 1 || take;
+      const float inv = lt > 0.f ? 1.f / lt : 0.f;
       if (d.parts == 1) {
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
         a0 *= inv;
         a1 *= inv;
       }
+      // four elements of this part with the other's, as the merge adds them
+      auto add_other = [&](float* x, int col) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w_with > 0.f) y = __ldcg(with + col / 4 * p.slot_rows);
+        const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = inv * (own_first ? two_parts(x[i], w_own, z[i], w_with)
+                                  : two_parts(z[i], w_with, x[i], w_own));
+      };
       uint16_t* out = static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride +
                       head * p.out.head_stride + c0;
       if constexpr (QUAD) {
@@ -1268,7 +1323,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           if (valid) {
             const int col = c * SW + (warp & 3) * kOwn;
-            if (d.parts == 1) {
+            if (whole) {
               uint32_t u[kOwn / 2];
 #pragma unroll
               for (int i = 0; i < kOwn / 2; ++i) u[i] = pack2<F16>(o[2 * i], o[2 * i + 1]);
@@ -1308,7 +1363,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (some0) add(at, a0);
             if (some1) add(at + 128, a1);
           }
-          if (d.parts > 1) {
+          if (kTakes && take) {
+#pragma unroll
+            for (int i = 0; i < kC; i += 4) add_other(v + i, c0 + c * kC + i);
+          }
+          if (!whole) {
             if (valid && lt > 0.f) {
 #pragma unroll
               for (int i = 0; i < kC; i += 4)
@@ -1344,11 +1403,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) mbar_arrive(o_empty);
       }
       if (valid && (PAIR || warp == 0 || (!QUAD && wg == 0))) {
-        if (d.parts > 1)
+        if (!whole)
           p.part_ml[(size_t)d.slot * p.slot_rows + part_row] = make_float2(mt, lt);
         else if (p.lse != nullptr)
-          p.lse[(size_t)r * p.Hq + head] =
-              lt > 0.f ? 0.6931471805599453f * mt + logf(lt) : -INFINITY;
+          p.lse[(size_t)r * p.Hq + head] = log_sum(mt, lt);
+      }
+      if (kTakes && take) {
+        if (t == 0) p.ready[d.first] = epoch | 1;  // nothing is left to merge
+      } else if (kTakes && d.parts == 2) {  // announce this part
+        __threadfence();
+        named_bar_sync(1, 256);
+        if (t == 0) st_release_gpu(p.ready + d.first, epoch);
       }
     }
   }
@@ -1400,10 +1465,10 @@ struct RowSum {
     const float mn = fmaxf(m, ml.x);
     const float a = fast_exp2(m - mn), b = fast_exp2(ml.x - mn);
     m = mn;
-    l = l * a + ml.y * b;
+    l = two_parts(l, a, ml.y, b);
     const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * a + v[i] * b;
+    for (int i = 0; i < 8; ++i) o[i] = two_parts(o[i], a, v[i], b);
   }
 };
 
@@ -1419,7 +1484,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
   grid_dep_launch();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int4 cut = t < kNumSMs ? p.cut[t] : make_int4(0, 0, 0, 0);
-  const bool is = (cut.w & 0xffff) > 1;
+  const int ready = t < kNumSMs ? p.ready[t] : 0;
+  const bool is = (cut.w & 0xffff) > 1 && ready != (cut.z | 1);
+  if (blockIdx.x == 0 && t == 0) *p.epoch += 2;  // what is announced now is old
   const unsigned mask = __ballot_sync(0xffffffffu, is);
   if (lane == 0) counts[warp] = __popc(mask);
   __syncthreads();
@@ -1432,7 +1499,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
   if (n == 0) return;
   if (is)
     tiles[before] =
-        make_int4(cut.x, cut.y | cut.z << 12, cut.w & 0xffff, 2 * t + (cut.w >> 16));
+        make_int4(cut.x, cut.y, cut.w & 0xffff, 2 * t + (cut.w >> 16));
   __syncthreads();
   const int rows32 = (p.slot_rows + 31) / 32;  // warps for the rows of a tile
   const int per_tile = D / 8 * rows32;
@@ -1487,13 +1554,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
       uint16_t* out =
           static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride + head * p.out.head_stride;
       *reinterpret_cast<uint4*>(out + 8 * col8) =
-          make_uint4(pack2<F16>(sum.o[0] * inv, sum.o[1] * inv),
-                     pack2<F16>(sum.o[2] * inv, sum.o[3] * inv),
-                     pack2<F16>(sum.o[4] * inv, sum.o[5] * inv),
-                     pack2<F16>(sum.o[6] * inv, sum.o[7] * inv));
+          make_uint4(pack2<F16>(inv * sum.o[0], inv * sum.o[1]),
+                     pack2<F16>(inv * sum.o[2], inv * sum.o[3]),
+                     pack2<F16>(inv * sum.o[4], inv * sum.o[5]),
+                     pack2<F16>(inv * sum.o[6], inv * sum.o[7]));
       if (col8 == 0 && p.lse != nullptr)
-        p.lse[(size_t)r * p.Hq + head] =
-            sum.l > 0.f ? 0.6931471805599453f * sum.m + logf(sum.l) : -INFINITY;
+        p.lse[(size_t)r * p.Hq + head] = log_sum(sum.m, sum.l);
     }
   }
 }

@@ -95,8 +95,10 @@ int query_tiles(int n_rows, int items, int G) {
   return rows <= 32 ? kPagedQuad : rows > 144 ? kPagedPair : kPagedSplit;
 }
 
-// Workspace: status word, a record per CTA, the parts of cut query tiles.
-constexpr size_t kWsCut = 256, kWsParts = 4096;
+// Workspace: status word, launch epoch and announcements of parts (cleared once),
+// a record per CTA, the parts of cut query tiles.
+constexpr size_t kWsEpoch = 64, kWsReady = 256, kWsCut = 1024, kWsParts = 4096;
+static_assert(kWsReady + sizeof(int) * kNumSMs <= kWsCut, "the announcements fit");
 static_assert(kWsCut + sizeof(int4) * kNumSMs <= kWsParts, "the records fit before the parts");
 
 int slot_rows(long long n_rows, int G) {
@@ -188,6 +190,8 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
   p.scale_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.f / sqrtf((float)D));
   p.lse = lse;
   p.status = static_cast<int*>(ws);
+  p.epoch = reinterpret_cast<int*>(w + kWsEpoch);
+  p.ready = reinterpret_cast<int*>(w + kWsReady);
   p.cut = reinterpret_cast<int4*>(w + kWsCut);
   p.part = reinterpret_cast<float*>(w + kWsParts);
   p.part_ml = reinterpret_cast<float2*>(p.part + (size_t)2 * kNumSMs * p.slot_rows * D);
@@ -268,7 +272,7 @@ dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream str
   if (ws_bytes < kWsParts) return DLLM_ERR_WORKSPACE;
   const dllm_status e = prepare_device();  // so that the first attention may be a captured one
   if (e != DLLM_OK) return e;
-  return cudaMemsetAsync(ws, 0, 256, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return cudaMemsetAsync(ws, 0, kWsCut, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? DLLM_OK
              : DLLM_ERR_CUDA;
 }
