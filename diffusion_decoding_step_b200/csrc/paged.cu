@@ -432,6 +432,20 @@ DLLM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abor
   return __all_sync(0xffffffffu, ok);
 }
 
+// Warps meet at a barrier that counts one arrival of each; false when the watchdog
+// gave up.  (At a hardware barrier they would wait for warps that have left.)
+struct Meeting {
+  uint64_t* bar;
+  uint32_t parity = 0;
+  DLLM_DEV bool join(int lane, const volatile int* abort) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    const bool ok = warp_wait(bar, parity, abort);
+    parity ^= 1;
+    return ok;
+  }
+};
+
 // Sum over the block's threads before this one (all threads; scratch of one
 // entry per warp).
 DLLM_DEV int block_before(int v, int* scratch, int warp, int lane) {
@@ -491,7 +505,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* q_empty = q_full + 1;
   uint64_t* o_full = q_empty + 1;
   uint64_t* o_empty = o_full + 1;
-  uint64_t* done = o_empty + 1;
+  uint64_t* meet = o_empty + 1;  // both streams; each one
+  uint64_t* done = meet + 3;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* progress = abort + 1;
@@ -522,6 +537,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     mbar_init(q_empty, 1);
     mbar_init(o_full, 1);
     mbar_init(o_empty, 8);
+    mbar_init(&meet[0], 8);
+    mbar_init(&meet[1], 4);
+    mbar_init(&meet[2], 4);
     mbar_init(done, 11);
     *abort = 0;
     *progress = 0;
@@ -713,11 +731,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         sg = seq_segs(p, i);
         own_total = seg_tiles(sg);
       }
+      // the largest limit of the rows from a to b
+      auto rows_limit = [&](int a, int b) {
+        int lim = 0;
+#pragma unroll 1
+        for (int r = a + lane; r < b; r += 32) lim = max(lim, p.row_limit[r]);
+        return __reduce_max_sync(0xffffffffu, lim);
+      };
+      // limit of sequence lim_s in this query tile: a slot beyond it is treated like
+      // one outside the segments, and may hold anything
+      int lim = INT_MAX, lim_s = s_first;
       if (p.row_limit != nullptr && rs[s_first + 1] >= r0 + nrows) {
         // all rows of one sequence: its last tiles may be beyond every row's limit
-        int lim = 0;
-        for (int r = lane; r < nrows; r += 32) lim = max(lim, p.row_limit[r0 + r]);
-        lim = __reduce_max_sync(0xffffffffu, lim);
+        lim = rows_limit(r0, r0 + nrows);
         Segs s0 = sg;
         if constexpr (GROUPS)
           s0 = Segs{__shfl_sync(0xffffffffu, sg.a0, 0), __shfl_sync(0xffffffffu, sg.e0, 0),
@@ -798,9 +824,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         Loc c;
         Segs x = sg;
         const int* table = p.bt.table + (size_t)i * p.bt.table_stride;
-        int kk = k;
+        int kk = k, own_lim = INT_MAX;
         if constexpr (!GROUPS) {
           c.w = nrows << 9 | 1 << 18;
+          own_lim = lim;
         } else if (k < ktp) {
           x = Segs{0, pk[g], 0, 0};
           table = p.ptable + (size_t)g * p.ptable_stride;
@@ -818,9 +845,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           kk = o - own_before - __shfl_sync(0xffffffffu, incl - kt, l);
           const int s = sb + l;
           table = p.bt.table + (size_t)s * p.bt.table_stride;
-          c.w = max(rs[s] - r0, 0) | min(rs[s + 1] - r0, nrows) << 9 | 1 << 18;
+          const int from = max(rs[s] - r0, 0), to = min(rs[s + 1] - r0, nrows);
+          c.w = from | to << 9 | 1 << 18;
+          if (p.row_limit != nullptr && (s != lim_s || lim == INT_MAX)) {
+            lim = rows_limit(r0 + from, r0 + to);
+            lim_s = s;
+          }
+          own_lim = lim;
         }
         key_tile(x, kk, c.kb, c.kl, c.kh);
+        c.kh = min(c.kh, own_lim);
         c.page = p.kv.n_pages;
         const int at = c.kb + lane * page_keys;
         if (lane < page_boxes && at < c.kh && at + page_keys > c.kl) {
@@ -996,6 +1030,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int page_keys = min(kKeyTile, 1 << p.kv.page_shift);
     int n_piece = 0, n_q = 0, s_cnt = 0, n_tile = 0, n_two = 0;
     const int epoch = kTakes ? *p.epoch + 2 : 0;
+    Meeting all{meet}, own_wg{meet + 1 + wg};
     bool ok = true;
     while (ok) {
       const int qi = n_piece % kQueue;
@@ -1191,7 +1226,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (kTakes && d.parts == 2) {
         volatile int* there = other_s + (n_two++ & 1);
         if (t == 0) *there = ld_acquire_gpu(p.ready + d.first) == epoch;
-        named_bar_sync(1, 256);
+        ok = all.join(lane, abort);
+        if (!ok) break;
         take = uniform(*there);
       }
       float a0 = 1.f, a1 = 0.f, mt = m, lt = l;
@@ -1199,7 +1235,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if constexpr (!PAIR) {  // (max, sum) of both streams; each takes half of the columns
           float2* x = reinterpret_cast<float2*>(x_s) + (n_q & 1) * 256;
           x[wg * 128 + row] = make_float2(m, l);
-          named_bar_sync(1, 256);
+          ok = all.join(lane, abort);
+          if (!ok) break;
           const float2 y0 = x[row], y1 = x[128 + row];  // a stream without tiles has sum 0
           mt = fmaxf(y0.x, y1.x);
           if constexpr (QUAD) {
@@ -1297,12 +1334,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(o_empty);
           }
-          named_bar_sync(2 + wg, 128);  // the buffer is free
+          ok = own_wg.join(lane, abort);  // the buffer is free
+          if (!ok) break;
 #pragma unroll
           for (int k = 0; k < SW / 4; ++k)
             ms[((warp & 3) * (SW / 4) + k) * 32 + lane] =
                 make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          named_bar_sync(2 + wg, 128);
+          ok = own_wg.join(lane, abort);
+          if (!ok) break;
           float o[kOwn];
 #pragma unroll
           for (int k = 0; k < kOwn / 4; ++k) {
@@ -1412,8 +1451,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (t == 0) p.ready[d.first] = epoch | 1;  // nothing is left to merge
       } else if (kTakes && d.parts == 2) {  // announce this part
         __threadfence();
-        named_bar_sync(1, 256);
-        if (t == 0) st_release_gpu(p.ready + d.first, epoch);
+        ok = all.join(lane, abort);
+        if (ok && t == 0) st_release_gpu(p.ready + d.first, epoch);
       }
     }
   }

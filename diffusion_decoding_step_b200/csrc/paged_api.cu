@@ -148,7 +148,8 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
   if (e == DLLM_OK) e = check_heads(n_q_heads, p.kv);
   if (e != DLLM_OK) return e;
   if (!segs || !aligned4(segs) || !aligned4(row_limit) || !aligned4(lse)) return DLLM_ERR_INVALID;
-  if (!(scale >= 0.f && scale <= FLT_MAX)) return DLLM_ERR_INVALID;  // NaN, inf, negative
+  // NaN, inf, negative; in log2 units it has to be finite as well
+  if (!(scale >= 0.f && scale <= 0x1p127f)) return DLLM_ERR_INVALID;
   if (!rows_ok(q, p.bt.n_rows, n_q_heads, p.kv.D, &p.q) ||
       !rows_ok(out, p.bt.n_rows, n_q_heads, p.kv.D, &p.out) || q->data == out->data)
     return DLLM_ERR_INVALID;

@@ -37,7 +37,8 @@ class PagedKV:
 
     Calls run on the current stream of the pages' device and return without waiting.  The
     attention calls share one workspace: a PagedKV serves one of them at a time, and graphs or
-    streams that may overlap each take a PagedKV of their own over the same pages.
+    streams that may overlap each take a PagedKV of their own over the same pages.  Keep the
+    object until its calls have run: the workspace's memory goes with it.
     """
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, n_q_heads: int,
@@ -69,6 +70,8 @@ class PagedKV:
             stream = torch.cuda.current_stream(self.device).cuda_stream
             abi.check(abi.dllm_paged_workspace_init(self.ws.data_ptr(), n.value, stream),
                       "paged_workspace_init")
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()  # calls may come on any stream
         fns = (C.cast(f, C.c_void_p).value for f in (lib.dllm_paged_append, lib.dllm_paged_attn,
                                                      lib.dllm_shared_prefix_attn))
         self._append, self._attn = binding.append, binding.attn

@@ -420,7 +420,8 @@ dllm_status dllm_paged_append(const dllm_kv_pages* kv, const dllm_paged_batch* b
 dllm_status dllm_paged_workspace_size(const dllm_kv_pages* kv, int32_t n_q_heads,
                                       int32_t max_rows, size_t* bytes);
 
-/* Clear the workspace's status word (256-byte aligned ws); once per workspace.
+/* Clear the workspace's status word and bookkeeping (256-byte aligned ws); once
+ * per workspace, before the calls that use it.
  * dllm_device_status reads the word.  A workspace serves one call at a time. */
 dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream stream);
 
@@ -433,9 +434,11 @@ dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream str
  * h / (n_q_heads / n_kv_heads); scores are scaled by `scale` (0: 1/sqrt(D)).
  * out[r][h] = softmax-weighted values; lse[r][h] (fp32 [n_rows][n_q_heads],
  * NULL: not wanted) = the natural log of the sum of exponentials.  A row that
- * sees nothing gets out = 0 and lse = -inf.  Slots outside every segment may
- * hold anything, infinities and NaN included; inside the segments the values
- * must be finite wherever any row of the sequence could read them.
+ * sees nothing gets out = 0 and lse = -inf.  Slots that no row sees (outside
+ * the segments, or beyond the limits of all rows) may hold anything, infinities
+ * and NaN included; what some row sees must be finite, since rows that do not
+ * see it are multiplied with it as well, at weight zero.  scale is at most
+ * 2^127.
  * out must not overlap q. */
 dllm_status dllm_paged_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
                             int32_t n_q_heads, const int32_t* segs, const int32_t* row_limit,

@@ -208,8 +208,9 @@ def test_append_any_row_start_stays_in_bounds():
 
 # ------------------------------------------------------------------ attention
 def run_attn(dtype, D, hq, hkv, ps, layout, rows, segs, limit=None, groups=None, scale=0.0, seed=0,
-             before=1, behind=2, nan=True, width=None, kv_rows=None, spread=1.0, caps=None):
-    """groups: (first sequences, prefix lengths)."""
+             before=1, behind=2, nan=True, width=None, kv_rows=None, spread=1.0, caps=None, seen_only=False):
+    """groups: (first sequences, prefix lengths).  seen_only: slots beyond the limits of all rows
+    hold anything too."""
     g = _gen(seed + 13 * D + ps + sum(rows))
     top = [max([0] + [a + n for a, n in sg if n > 0]) for sg in segs]
     pre = groups[1] if groups else []
@@ -224,6 +225,8 @@ def run_attn(dtype, D, hq, hkv, ps, layout, rows, segs, limit=None, groups=None,
         used = torch.zeros(n_pages, ps, dtype=torch.bool)
         for s, sg in enumerate(segs):
             p = R.seq_positions(sg, table.shape[1] * ps)
+            if seen_only:
+                p = p[p < max([0] + [limit(s, j) for j in range(rows[s])])]
             used[table[s][p // ps].long(), p % ps] = True
         for i, n in enumerate(pre):
             p = torch.arange(n)
@@ -307,6 +310,21 @@ def test_attn_row_limits(case, mask):
          "random": lambda s, j: rng.choice([0, 1, -7, 2 ** 31 - 1, rng.randint(0, end[s] + 3)]),
          "nothing": lambda s, j: 0}[mask]
     run_attn(*case, limit=f)
+
+
+@pytest.mark.parametrize("case", [
+    (BF, 128, 28, 4, 16, "heads", [1, 3, 2], whole(300, 129, 128)),       # 32-row tiles
+    (HF, 128, 8, 8, 64, "slots", [40, 100, 33], whole(300, 700, 64)),      # 128-row tiles
+    (BF, 64, 8, 2, 256, "heads", [90, 300], whole(900, 400)),              # 256-row tiles
+], ids=lambda c: str(c)[:60])
+def test_slots_beyond_all_limits_hold_anything(case):
+    lens = [sg[0][1] for sg in case[7]]
+    for back in (1, 100):       # the last key seen is `back` before the segment's end
+        run_attn(*case, limit=lambda s, j: lens[s] - back - j % 3, seen_only=True)
+    run_attn(*case, limit=lambda s, j: 0 if s == 1 else 5, seen_only=True)
+    n = len(lens)
+    run_attn(*case, limit=lambda s, j: lens[s] - 7 * (s + 1) - j % 2, seen_only=True,
+             groups=([0, n - 1, n], [70, 0]))
 
 
 def test_attn_scale_and_large_scores():
@@ -616,6 +634,7 @@ def test_arguments_are_checked():
         lambda: kv.attn(q, rs, tab, segs, out=q),
         lambda: kv.attn(q, rs, tab, segs, scale=-1.0),
         lambda: kv.attn(q, rs, tab, segs, scale=math.nan),
+        lambda: kv.attn(q, rs, tab, segs, scale=3e38),
         lambda: kv.append(k, k, rs, tab, pos, rope_theta=math.inf),
         lambda: PagedKV(pool[0], pool[1], 3, 3),
         lambda: PagedKV(pool[0][:, :, :12], pool[1][:, :, :12], 4, 3),
