@@ -322,19 +322,14 @@ struct PagedAttnParams {
   int G, rows_per_tile;  // query heads per kv head; rows of a query tile
   // workspace: parts of cut query tiles, a CTA's two slots of slot_rows rows
   // [2 * kNumSMs][slot_rows][D] with their (max, sum), and the cut tile that
-  // starts in a CTA [kNumSMs]: first row, rows | kv head << 12, epoch, parts |
-  // slot parity << 16.  epoch: even, two more with every launch; ready [kNumSMs]
-  // of a tile of two parts by its first CTA: epoch when one part is announced,
-  // epoch | 1 once the tile is written out.  (An old entry could be taken for a
-  // new one after 2^31 launches that never cut a tile there.)
+  // starts in a CTA [kNumSMs]: first row, rows | kv head << 12, parts, first slot
   int slot_rows;
   float* part;
   float2* part_ml;
   int4* cut;
-  int *epoch, *ready;
 };
-// Query tiles of 128 rows, of 256 rows, of 32 rows (paged.cu says how they work).
-enum PagedMode : int { kPagedSplit = 0, kPagedPair = 1, kPagedQuad = 2 };
+// Query tiles of 128 rows, of 32 rows (paged.cu says how they work).
+enum PagedMode : int { kPagedSplit, kPagedQuad };
 cudaError_t paged_attn_prepare();
 cudaError_t launch_paged_attn(const CUtensorMap& qmap, const CUtensorMap& kmap,
                               const CUtensorMap& vmap, const PagedAttnParams& p, int mode,

@@ -68,7 +68,9 @@ DLLM_DEV Segs seq_segs(const PagedAttnParams& p, int s) {
 // bits, so that far positions keep their fraction of a turn.  Meanwhile the block's
 // threads already load 2 x 16 bytes of a head each, several heads at a time:
 // elements i.. and i + D/2.., which the rotation pairs.  The operator is bound by
-// its bytes; a few rows by the two dependent loads (sequence, page).
+// its bytes: 9.7 thousand rows of 28 + 2 x 4 heads 38.1 us, 179 MB, 4.7 TB/s of a
+// copy's 6.5; 512 rows of 96 heads 6.6 us, 3.8 TB/s.  A few rows are bound by the two
+// dependent loads (sequence, page): one row 3.2 us.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = 8;   // most rows of a block, one for each warp
 
@@ -270,6 +272,19 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 // the other rows do not see.  Key tiles are aligned to 128 positions, so a tile
 // is a whole number of pages or lies inside one.
 //
+// Mathematics: out = sum_k exp(x_k - m) v_k / sum_k exp(x_k - m), x_k = scale q.k, in
+// one pass with a running maximum m and sum in fp32; x is taken in log2 units.  P is
+// rounded to the cache's type for the second product (half a step each, as its
+// input type demands), the sum takes it unrounded.
+//
+// What bounds it, measured: few query rows by the keys' bytes (a token each of 32
+// sequences, 28 heads over 4, 270 MB: 57 us, 4.9 TB/s; one token over 131,001 keys
+// 54.5 us, the same rate; blocks of 32 rows of 16 sequences, 32 heads, 278 MB: 60 us,
+// 4.7 TB/s; in the steady state 6 TB/s, the rest is the start and the merge); many
+// by the products and the softmax between them (32 blocks of 32 rows that share 8192
+// keys 140 us, 890 TFLOP/s; two chunks of 1024 rows at 2 to 4 thousand keys 90 us,
+// 630); short ones by latency (32 rows over 544 keys 14 us).
+//
 // All query tiles of all items and kv heads, each with its key tiles plus a
 // fixed cost, form one line that the CTAs (one per SM) cut into equal shares,
 // whatever the lengths on the device are.  Every CTA finds its share itself by
@@ -281,17 +296,17 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //   warps 8, 10 walk the share and load K (with Q) and V through TMA; each lane
 //               fetches its page's table entry and issues that page's boxes (one
 //               warp alone could not issue the boxes of 16-slot pages in time:
-//               32 tokens over small pages 81 us, with two 63).  Pages without a
+//               32 tokens over small pages took 81 us, with two 63).  Pages without a
 //               key of the tile are requested past the last page, which TMA fills
 //               with zeros without reading.  Warp 8 also describes pieces and key
 //               tiles in two small queues.
 //   warp 9      issues S = Q K^T and O += P V on tcgen05.  (One warp for each stream
 //               let the streams' products interleave and their softmaxes run at the
-//               same time: 187 us instead of 161 for the 32 samples.)
+//               same time: 187 us where one warp took 161 for the 32 blocks.)
 //   warp 11     is the watchdog: the waits of the others are unbounded until it finds
 //               that nothing was multiplied for two seconds, reports that and lets
 //               them go.  (A clock in every wait made the code a tenth longer, and a
-//               launch pays for its code: it is fetched anew.)
+//               launch pays for its code, which it fetches anew.)
 //   warps 0-3 and 4-7   softmax of two streams with their own S, P and O in
 //               TMEM, so that the products of one run during the softmax of the
 //               other.  A thread owns a query row; P overwrites S in TMEM as the
@@ -300,9 +315,10 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //               stale, which the final division cancels).
 // Query tiles and streams:
 //   kSplit  128 rows; the streams take key tiles in turn and are merged at the
-//           end of a piece.
-//   kPair   256 rows; the streams are its two halves, which share every K and V
-//           tile.
+//           end of a piece.  (256 rows, a half for each stream, share K and V but
+//           halve the number of tiles to spread: 32 rows over 544 keys 15.9 us
+//           instead of 14.0, 32 blocks 144 instead of 140, the prompt chunks 87
+//           instead of 90.)
 //   kQuad   32 rows, in four copies on the 128 lanes of TMEM; the streams take key
 //           tiles in turn, and warp w of a stream takes the w-th quarter
 //           of a tile's keys alone (P is zero elsewhere in its copy), so a tile
@@ -311,27 +327,19 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //
 // A query tile that one CTA did alone is written out.  The parts of a cut tile
 // go to the workspace in fp32, and a second kernel merges them in the order of
-// the keys.  Most cut tiles have two parts, the end of one CTA's share and the
-// start of the next one's, which is done long before: with 256-row tiles, whose
-// parts are large, a CTA that finds the other part of its tile announced takes it
-// from the workspace and writes the tile out, so that half the parts are never
-// written and the second kernel has little to do (prompt chunks 92 -> 86 us; with
-// the smaller tiles looking costs more than it saves, 32 tokens 57 -> 60).  Nothing waits for a part; where both CTAs miss the
-// other's, the second kernel does that tile as well.  Whoever adds two parts up
-// rounds in the same places, so results do not depend on who comes first.
+// the keys.
 constexpr int kKeyTile = 128;
 constexpr int kAttnThreads = 384;
 constexpr int kMaxSeqs = 1024;
 constexpr int kQueue = 4, kTileQueue = 8;
 constexpr float kGrow = 8.f;  // log2 of the growth of a maximum that rescales O
 constexpr int kTileCost = 2;  // fixed cost of a query tile, in key tiles
-constexpr int kSplit = kPagedSplit, kPair = kPagedPair, kQuad = kPagedQuad;
+constexpr int kSplit = kPagedSplit, kQuad = kPagedQuad;
 
 struct Piece {
   int r0, nrows, kvh, n;        // first row, rows, kv head, key tiles (-1: no more pieces)
   int parts;                    // parts of the query tile
   int slot;                     // partial slot: 2 * CTA, + 1 where it is not the CTA's first piece
-  int first, other;             // two parts: CTA of the first one; slot of the other one
 };
 
 template <int D, int MODE>
@@ -345,13 +353,12 @@ struct PagedCfg {
   static constexpr int kNBox = D / kBoxD;
   static constexpr int kBoxBytes = 128 * kRowBytes;
   static constexpr int kTile = 128 * D * 2;  // bytes of a Q, K or V tile
-  static constexpr int kQ = MODE == kPair ? 2 : 1;  // query tiles of 128 rows
   static constexpr int kMerge = MODE == kQuad ? 2 * 128 * (D < 64 ? 16 : 32) * 4 : 0;
   // prefix sums of the units, row and group starts, prefix lengths, group of each
   // sequence
   static constexpr int kPlan = 4 * (kMaxSeqs + 4) * 4 + kMaxSeqs * 2;
   static constexpr int kX = 4096;  // (max, sum) of both streams, for two pieces
-  static constexpr size_t kSmem = 1024 + (kQ + kSTK + kSTV) * kTile + kMerge + kPlan + kX +
+  static constexpr size_t kSmem = 1024 + (1 + kSTK + kSTV) * kTile + kMerge + kPlan + kX +
                                   kQueue * sizeof(Piece) + kTileQueue * 16 + 512;
 };
 
@@ -387,12 +394,8 @@ struct Shares {
   }
 };
 
-// Two parts by their weights, rounded in the same places wherever it is done.
-DLLM_DEV float two_parts(float x, float wx, float y, float wy) {
-  return __fmaf_rn(y, wy, __fmul_rn(x, wx));
-}
 DLLM_DEV float log_sum(float m, float l) {  // of a maximum in log2 units and a sum
-  return l > 0.f ? __fmaf_rn(0.6931471805599453f, m, logf(l)) : -INFINITY;
+  return l > 0.f ? fmaf(0.6931471805599453f, m, logf(l)) : -INFINITY;
 }
 
 // Transpose of N units of 16 bytes among N neighbouring lanes (N = 2 or 4): after it
@@ -473,14 +476,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                       const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ PagedAttnParams p) {
   using C = PagedCfg<D, MODE>;
-  constexpr bool PAIR = MODE == kPair, QUAD = MODE == kQuad;
-  constexpr bool kTakes = PAIR;  // whether a CTA may finish a tile of two parts
+  constexpr bool QUAD = MODE == kQuad;
   constexpr int STK = C::kSTK, STV = C::kSTV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
   uint8_t* q_s = base_s;
-  uint8_t* k_s = q_s + C::kQ * C::kTile;  // [STK]
+  uint8_t* k_s = q_s + C::kTile;          // [STK]
   uint8_t* v_s = k_s + STK * C::kTile;    // [STV]
   float4* merge_s = reinterpret_cast<float4*>(v_s + STV * C::kTile);  // [2][4][SW / 4][32]
   int* upfx = reinterpret_cast<int*>(v_s + STV * C::kTile + C::kMerge);  // [n_seqs + 1]
@@ -510,10 +512,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* progress = abort + 1;
-  volatile int* other_s = progress + 1;  // [2]
 
   const int t = threadIdx.x, warp = uniform(t >> 5), lane = t & 31;
-  const int tile_rows = p.rows_per_tile * C::kQ;
+  const int tile_rows = p.rows_per_tile;
   if (t == 0) {
     for (int i = 0; i < STK; ++i) {
       mbar_init(&k_full[i], 1);
@@ -663,7 +664,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       u1 = sh.start(cta + 1);
     }
     int4 cut = make_int4(0, 0, 0, 0);
-    const int epoch = kTakes ? *p.epoch + 2 : 0;
     int i = 0, hi = n_seqs;  // the last sequence that starts at or before u
     while (hi - i > 1) {
       const int mid = (i + hi) / 2;
@@ -781,13 +781,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ok = n_piece < kQueue ||
              warp_wait(&d_empty[qi], (n_piece / kQueue - 1) & 1, abort);
         if (ok && lane == 0) {
-          Piece d{r0, nrows, kvh, n, 1, 2 * cta + (first_piece ? 0 : 1), cta, 0};
+          Piece d{r0, nrows, kvh, n, 1, 2 * cta + (first_piece ? 0 : 1)};
           if (x0 > start + kTileCost || x1 < end) {
-            d.first = sh.owner(start + kTileCost);
-            d.parts = sh.owner(end - 1) - d.first + 1;
-            d.other = d.first == cta ? 2 * (cta + 1) : 2 * d.first + (sh.start(d.first) < start);
-            if (d.first == cta)  // (lane 0's)
-              cut = make_int4(r0, nrows | kvh << 12, epoch, d.parts | (d.slot & 1) << 16);
+            const int first = sh.owner(start + kTileCost);
+            d.parts = sh.owner(end - 1) - first + 1;
+            if (first == cta) cut = make_int4(r0, nrows | kvh << 12, d.parts, d.slot);  // (lane 0's)
           }
           queue[qi] = d;
           mbar_arrive(&d_full[qi]);
@@ -802,16 +800,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ok = n_q == 0 || warp_wait(q_empty, (n_q - 1) & 1, abort);
         const int q_row = uniform(r0), q_head = uniform(kvh) * p.G;
         if (ok && elect_one()) {
-          constexpr int kCopies = QUAD ? 4 : C::kQ;
+          constexpr int kCopies = QUAD ? 4 : 1;
           mbar_arrive_expect_tx(q_full,
                                 kCopies * C::kNBox * p.G * p.rows_per_tile * C::kRowBytes);
 #pragma unroll
           for (int h = 0; h < kCopies; ++h)
 #pragma unroll
             for (int b = 0; b < C::kNBox; ++b)
-              tma_load_3d(q_s + h * (QUAD ? 32 * C::kRowBytes : C::kTile) + b * C::kBoxBytes,
-                          &qmap, q_full, b * C::kBoxD, q_head,
-                          q_row + (QUAD ? 0 : h * p.rows_per_tile));
+              tma_load_3d(q_s + h * 32 * C::kRowBytes + b * C::kBoxBytes, &qmap, q_full,
+                          b * C::kBoxD, q_head, q_row);
         }
       }
       ++n_q;
@@ -928,7 +925,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ok = warp_wait(&d_full[qi], (n_piece / kQueue) & 1, abort);
         if (!ok) break;
         const int n = uniform(queue[qi].n);
-        const bool two = uniform(queue[qi].nrows) > p.rows_per_tile;  // rows in both halves
         if (elect_one()) mbar_arrive(&d_empty[qi]);
         ++n_piece;
         if (n < 0) break;
@@ -941,29 +937,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int ti = n_tile + j;
           return warp_wait(&v_full[ti % STV], (ti / STV) & 1, abort);
         };
-        // S of key tile j in stream x; after the last use K (and Q) are free
-        auto s_mma = [&](int x, int j, bool last) {
+        // S of key tile j in stream x; then K (and after the last tile Q) is free
+        auto s_mma = [&](int x, int j) {
           const int st = (n_tile + j) % STK;
           const uint64_t kd = k_desc + (uint64_t)(st * C::kTile >> 4);
-          const uint64_t qd = q_desc + (uint64_t)(PAIR ? x * C::kTile >> 4 : 0);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               constexpr int kPerBox = C::kBoxD / 16;
               const int off = (kk / kPerBox) * C::kBoxBytes + (kk % kPerBox) * 32;
-              umma_bf16(tmem + x * 128, qd + (off >> 4), kd + (off >> 4), kIdS, kk > 0);
+              umma_bf16(tmem + x * 128, q_desc + (off >> 4), kd + (off >> 4), kIdS, kk > 0);
             }
             umma_commit(&s_full[x]);
-            if (last) {
-              umma_commit(&k_empty[st]);
-              if (j == n - 1) umma_commit(q_empty);
-            }
+            umma_commit(&k_empty[st]);
+            if (j == n - 1) umma_commit(q_empty);
           }
           __syncwarp();
         };
         // O of stream x.  128-key rows have the second half of P ready first: where
         // the whole is not there yet, its products start.
-        auto pv_mma = [&](int x, int j, bool accumulate, bool last) {
+        auto pv_mma = [&](int x, int j, bool accumulate) {
           const int st = (n_tile + j) % STV;
           const uint64_t vd = v_desc + (uint64_t)(st * C::kTile >> 4);
           constexpr int kSteps = kKeyTile / 16;
@@ -986,30 +979,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             *progress = n_tile + j + 1;
             if constexpr (QUAD) steps(kSteps / 2, accumulate);
             steps(0, true);
-            if (last) umma_commit(&v_empty[st]);
+            umma_commit(&v_empty[st]);
           }
           __syncwarp();
           return true;
         };
         ok = warp_wait(q_full, n_q & 1, abort);
         if (!ok) break;
-        // Each turn takes P of a stream, multiplies it, and issues the stream's next S.
-        // Pairs: the streams by turns, each with every tile; else a tile a turn, the
-        // streams in turn from the one that the last piece did not end with.
-        const int b = PAIR ? 0 : n_tile & 1, streams = PAIR && !two ? 1 : 2;
-        const int turns = PAIR && two ? 2 * n : n;
+        // Each turn takes P of a key tile, multiplies it, and issues the S after the
+        // next in its stream.  The streams take turns, from the one that the last
+        // piece did not end with.
+        const int b = n_tile & 1;
 #pragma unroll 1
-        for (int i = -streams; ok && i < turns; ++i) {
-          const int x = streams == 1 ? 0 : (b + i) & 1;
-          const int j = PAIR && two ? i >> 1 : i, j_s = PAIR ? j + 1 : i + 2;
-          const bool last = !PAIR || x == streams - 1;  // the tile's last use
-          if (i == 0) ok = n_q == 0 || warp_wait(o_empty, (n_q - 1) & 1, abort);
-          if (ok && i >= 0)
-            ok = (PAIR && x == 1 || wait_v(j)) && pv_mma(x, j, PAIR ? j > 0 : j > 1, last);
-          if (ok && j_s < n) {
-            ok = (PAIR && x == 1) || wait_k(j_s);
+        for (int j = -2; ok && j < n; ++j) {
+          const int x = (b + j) & 1;
+          if (j == 0) ok = n_q == 0 || warp_wait(o_empty, (n_q - 1) & 1, abort);
+          if (ok && j >= 0) ok = wait_v(j) && pv_mma(x, j, j > 1);
+          if (ok && j + 2 < n) {
+            ok = wait_k(j + 2);
             tc_fence_after();
-            if (ok) s_mma(x, j_s, last);
+            if (ok) s_mma(x, j + 2);
           }
         }
         if (ok && elect_one()) umma_commit(o_full);
@@ -1024,12 +1013,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_off + wg * 128;
     const uint32_t o_tm = tmem + lane_off + 256;
-    const int qrow = QUAD ? lane : row;  // row of the query tile (of its half)
-    const int row_in = qrow / p.G, hh = qrow - row_in * p.G;
-    const int rr = row_in + (PAIR ? wg * p.rows_per_tile : 0);  // row within the query tile
+    const int qrow = QUAD ? lane : row;  // query row of the tile
+    const int rr = qrow / p.G, hh = qrow - rr * p.G;
     const int page_keys = min(kKeyTile, 1 << p.kv.page_shift);
-    int n_piece = 0, n_q = 0, s_cnt = 0, n_tile = 0, n_two = 0;
-    const int epoch = kTakes ? *p.epoch + 2 : 0;
+    int n_piece = 0, n_q = 0, s_cnt = 0, n_tile = 0;
     Meeting all{meet}, own_wg{meet + 1 + wg};
     bool ok = true;
     while (ok) {
@@ -1037,14 +1024,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       ok = warp_wait(&d_full[qi], (n_piece / kQueue) & 1, abort);
       if (!ok) break;
       const Piece d{uniform(queue[qi].r0), uniform(queue[qi].nrows), uniform(queue[qi].kvh),
-                    uniform(queue[qi].n), uniform(queue[qi].parts), uniform(queue[qi].slot),
-                    uniform(queue[qi].first), uniform(queue[qi].other)};
+                    uniform(queue[qi].n), uniform(queue[qi].parts), uniform(queue[qi].slot)};
       if (lane == 0) mbar_arrive(&d_empty[qi]);
       ++n_piece;
       if (d.n < 0) break;
-      const bool valid = row_in < p.rows_per_tile && rr < d.nrows;
+      const bool valid = rr < d.nrows;
       const bool active = __any_sync(0xffffffffu, valid);
-      const bool stream = !PAIR || wg == 0 || d.nrows > p.rows_per_tile;  // the half has rows
       const int r = d.r0 + rr;
       const int limit = valid && p.row_limit != nullptr ? p.row_limit[r] : INT_MAX;
       float m = -FLT_MAX, l = 0.f;
@@ -1068,8 +1053,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
       };
-      const int j0 = PAIR ? 0 : (wg ^ n_tile) & 1;  // split: the streams take tiles in turn
-      for (int j = j0; stream && j < d.n; j += PAIR ? 1 : 2) {
+      const int j0 = (wg ^ n_tile) & 1;  // the streams take tiles in turn
+      for (int j = j0; j < d.n; j += 2) {
         const int ti = n_tile + j;
         ok = warp_wait(&t_full[ti % kTileQueue], (ti / kTileQueue) & 1, abort);
         if (!ok) break;
@@ -1188,8 +1173,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           load_half(0, sa);
           F2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
           // P of 64 keys in 32 columns.  (A share of the exponentials as polynomials
-          // on the FMA pipe was slower: the 32 samples' 161 us became 168, 172 and 193
-          // with two, three and four of eight.)
+          // on the FMA pipe was slower: 161 us for the 32 blocks became 168, 172 and
+          // 193 with two, three and four of eight.)
           auto probs = [&](const float (&x)[kH], uint32_t (&pk)[32]) {
 #pragma unroll
             for (int i = 0; i < kH; i += 2) {
@@ -1217,87 +1202,52 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[wg]);
       }
       if (!ok) break;
-      // split: whether each stream had tiles
+      // whether each stream had tiles
       const bool some0 = d.n > 1 || (d.n == 1 && (n_tile & 1) == 0);
       const bool some1 = d.n > 1 || (d.n == 1 && (n_tile & 1) == 1);
       n_tile += d.n;
-      // ---- the piece's result; of a tile of two parts, whether the other one is there
-      bool take = false;
-      if (kTakes && d.parts == 2) {
-        volatile int* there = other_s + (n_two++ & 1);
-        if (t == 0) *there = ld_acquire_gpu(p.ready + d.first) == epoch;
+      // ---- the piece's result
+      float a0 = 1.f, a1 = 0.f, mt = m, lt = l;
+      if (d.n > 0) {  // (max, sum) of both streams; each takes half of the columns
+        float2* x = reinterpret_cast<float2*>(x_s) + (n_q & 1) * 256;
+        x[wg * 128 + row] = make_float2(m, l);
         ok = all.join(lane, abort);
         if (!ok) break;
-        take = uniform(*there);
-      }
-      float a0 = 1.f, a1 = 0.f, mt = m, lt = l;
-      if (d.n > 0) {
-        if constexpr (!PAIR) {  // (max, sum) of both streams; each takes half of the columns
-          float2* x = reinterpret_cast<float2*>(x_s) + (n_q & 1) * 256;
-          x[wg * 128 + row] = make_float2(m, l);
-          ok = all.join(lane, abort);
-          if (!ok) break;
-          const float2 y0 = x[row], y1 = x[128 + row];  // a stream without tiles has sum 0
-          mt = fmaxf(y0.x, y1.x);
-          if constexpr (QUAD) {
+        const float2 y0 = x[row], y1 = x[128 + row];  // a stream without tiles has sum 0
+        mt = fmaxf(y0.x, y1.x);
+        if constexpr (QUAD) {
 #pragma unroll
-            for (int k = 1; k < 4; ++k)
-              mt = fmaxf(mt, fmaxf(x[(row + 32 * k) & 127].x, x[128 + ((row + 32 * k) & 127)].x));
-            lt = 0.f;
+          for (int k = 1; k < 4; ++k)
+            mt = fmaxf(mt, fmaxf(x[(row + 32 * k) & 127].x, x[128 + ((row + 32 * k) & 127)].x));
+          lt = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {  // the same order in every warp
-              const float2 y = x[k * 32 + lane];
-              lt += y.y * fast_exp2(y.x - mt);
-            }
+          for (int k = 0; k < 8; ++k) {  // the same order in every warp
+            const float2 y = x[k * 32 + lane];
+            lt += y.y * fast_exp2(y.x - mt);
           }
-          a0 = fast_exp2(y0.x - mt);
-          a1 = fast_exp2(y1.x - mt);
-          if constexpr (!QUAD) lt = y0.y * a0 + y1.y * a1;
         }
+        a0 = fast_exp2(y0.x - mt);
+        a1 = fast_exp2(y1.x - mt);
+        if constexpr (!QUAD) lt = y0.y * a0 + y1.y * a1;
         ok = warp_wait(o_full, n_q & 1, abort);
         if (!ok) break;
         ++n_q;
         tc_fence_after();
       }
-      constexpr int kCols = PAIR ? D : D / 2;
+      constexpr int kCols = D / 2;
       constexpr int kC = kCols < 32 ? kCols : 32;
-      const int c0 = PAIR ? 0 : wg * kCols;
+      const int c0 = wg * kCols;
       const int head = d.kvh * p.G + hh;
       // a slot is [D / 4][slot_rows] groups of four elements: neighbouring rows are
       // neighbours, as in the lanes that write them
-      const int part_row = (PAIR ? wg * 128 : 0) + qrow;
       float4* part =
-          reinterpret_cast<float4*>(p.part) + (size_t)d.slot * p.slot_rows * (D / 4) + part_row;
-      const float4* with = reinterpret_cast<const float4*>(p.part) +
-                           (size_t)d.other * p.slot_rows * (D / 4) + part_row;
-      const bool own_first = d.first == (int)blockIdx.x;
-      float w_own = 1.f, w_with = 0.f;  // weights of the two parts
-      if (kTakes && take && valid) {
-        const float2 y = __ldcg(&p.part_ml[(size_t)d.other * p.slot_rows + part_row]);
-        if (y.y > 0.f) {
-          const float both = fmaxf(mt, y.x);
-          w_own = fast_exp2(mt - both);
-          w_with = fast_exp2(y.x - both);
-          lt = own_first ? two_parts(lt, w_own, y.y, w_with) : two_parts(y.y, w_with, lt, w_own);
-          mt = both;
-        }
-      }
-      const bool whole = d.parts == 1 || take;
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
-      if (d.parts == 1) {
+          reinterpret_cast<float4*>(p.part) + (size_t)d.slot * p.slot_rows * (D / 4) + qrow;
+      const bool whole = d.parts == 1;
+      if (whole) {
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
         a0 *= inv;
         a1 *= inv;
       }
-      // four elements of this part with the other's, as the merge adds them
-      auto add_other = [&](float* x, int col) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (w_with > 0.f) y = __ldcg(with + col / 4 * p.slot_rows);
-        const float z[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = inv * (own_first ? two_parts(x[i], w_own, z[i], w_with)
-                                  : two_parts(z[i], w_with, x[i], w_own));
-      };
       uint16_t* out = static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride +
                       head * p.out.head_stride + c0;
       if constexpr (QUAD) {
@@ -1396,16 +1346,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int i = 0; i < kC; ++i) v[i] = 0.f;
           const uint32_t at = o_tm + c0 + c * kC;
-          if constexpr (PAIR) {
-            if (d.n > 0) add(at + wg * 128, a0);
-          } else {
-            if (some0) add(at, a0);
-            if (some1) add(at + 128, a1);
-          }
-          if (kTakes && take) {
-#pragma unroll
-            for (int i = 0; i < kC; i += 4) add_other(v + i, c0 + c * kC + i);
-          }
+          if (some0) add(at, a0);
+          if (some1) add(at + 128, a1);
           if (!whole) {
             if (valid && lt > 0.f) {
 #pragma unroll
@@ -1441,18 +1383,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(o_empty);
       }
-      if (valid && (PAIR || warp == 0 || (!QUAD && wg == 0))) {
+      if (valid && (warp == 0 || (!QUAD && wg == 0))) {
         if (!whole)
-          p.part_ml[(size_t)d.slot * p.slot_rows + part_row] = make_float2(mt, lt);
+          p.part_ml[(size_t)d.slot * p.slot_rows + qrow] = make_float2(mt, lt);
         else if (p.lse != nullptr)
           p.lse[(size_t)r * p.Hq + head] = log_sum(mt, lt);
-      }
-      if (kTakes && take) {
-        if (t == 0) p.ready[d.first] = epoch | 1;  // nothing is left to merge
-      } else if (kTakes && d.parts == 2) {  // announce this part
-        __threadfence();
-        ok = all.join(lane, abort);
-        if (ok && t == 0) st_release_gpu(p.ready + d.first, epoch);
       }
     }
   }
@@ -1493,8 +1428,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // is eight elements of 32 rows of a tile (a lane a row, as the parts are stored), and
 // where there are fewer items than warps, several warps share an item's parts.  The
 // parts of a tile are in the slot of the CTA it starts in and in the even slots of
-// the CTAs after it; they are added in that order.  One resident wave of blocks: a
-// grid with blocks for every CTA that mostly find nothing took 2 to 5 us more.
+// the CTAs after it; they are added in that order.  Bound by latency: 4 to 5 us for
+// up to 38 MB of parts that are still in L2.  One resident wave of blocks: a grid
+// with blocks for every CTA that mostly find nothing took 2 to 5 us more.
 constexpr int kMergeWarps = 8, kMergeBlocks = 4 * kNumSMs;
 
 struct RowSum {
@@ -1504,10 +1440,10 @@ struct RowSum {
     const float mn = fmaxf(m, ml.x);
     const float a = fast_exp2(m - mn), b = fast_exp2(ml.x - mn);
     m = mn;
-    l = two_parts(l, a, ml.y, b);
+    l = l * a + ml.y * b;
     const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = two_parts(o[i], a, v[i], b);
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * a + v[i] * b;
   }
 };
 
@@ -1523,9 +1459,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
   grid_dep_launch();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int4 cut = t < kNumSMs ? p.cut[t] : make_int4(0, 0, 0, 0);
-  const int ready = t < kNumSMs ? p.ready[t] : 0;
-  const bool is = (cut.w & 0xffff) > 1 && ready != (cut.z | 1);
-  if (blockIdx.x == 0 && t == 0) *p.epoch += 2;  // what is announced now is old
+  const bool is = cut.z > 1;
   const unsigned mask = __ballot_sync(0xffffffffu, is);
   if (lane == 0) counts[warp] = __popc(mask);
   __syncthreads();
@@ -1536,9 +1470,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     n += counts[w];
   }
   if (n == 0) return;
-  if (is)
-    tiles[before] =
-        make_int4(cut.x, cut.y, cut.w & 0xffff, 2 * t + (cut.w >> 16));
+  if (is) tiles[before] = cut;
   __syncthreads();
   const int rows32 = (p.slot_rows + 31) / 32;  // warps for the rows of a tile
   const int per_tile = D / 8 * rows32;
@@ -1551,10 +1483,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     const int4 tile = tiles[ti];
     const int col8 = in_tile / rows32;
     const int at = (in_tile - col8 * rows32) * 32 + lane;
-    // 256-row tiles have 128 places for each half
-    const int half = at >> 7, in = at & 127;
-    const int rr = in / p.G + half * p.rows_per_tile, hh = in % p.G;
-    const bool have = item < items && in < p.rows_per_tile * p.G && rr < (tile.y & 0xfff);
+    const int rr = at / p.G, hh = at % p.G;
+    const bool have = item < items && rr < (tile.y & 0xfff);
     RowSum sum;
     if (have) {
       const float4* part = reinterpret_cast<const float4*>(p.part) + 2 * col8 * p.slot_rows + at;
@@ -1619,9 +1549,8 @@ cudaError_t launch_mode(const CUtensorMap& qm, const CUtensorMap& km, const CUte
 template <int D, bool F16>
 cudaError_t launch_paged_attn_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
                                 const PagedAttnParams& p, int mode, cudaStream_t s) {
-  const cudaError_t e = mode == kPair   ? launch_mode<D, F16, kPair>(qm, km, vm, p, s)
-                        : mode == kQuad ? launch_mode<D, F16, kQuad>(qm, km, vm, p, s)
-                                        : launch_mode<D, F16, kSplit>(qm, km, vm, p, s);
+  const cudaError_t e = mode == kQuad ? launch_mode<D, F16, kQuad>(qm, km, vm, p, s)
+                                      : launch_mode<D, F16, kSplit>(qm, km, vm, p, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged_merge_kernel<D, F16>, dim3(kMergeBlocks), dim3(kMergeWarps * 32), 0, s,
                     p);
@@ -1644,7 +1573,6 @@ cudaError_t prepare_mode() {
 template <int D, bool F16>
 cudaError_t prepare_t() {
   cudaError_t e = prepare_mode<D, F16, kSplit>();
-  if (e == cudaSuccess) e = prepare_mode<D, F16, kPair>();
   if (e == cudaSuccess) e = prepare_mode<D, F16, kQuad>();
   return e;
 }

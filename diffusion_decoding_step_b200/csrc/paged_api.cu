@@ -88,22 +88,22 @@ dllm_status check_heads(int n_q_heads, const PagedPool& kv) {
 
 // Query tiles by the average query rows of an item (a group, or a sequence
 // without one), rounded down since a padded batch has a few rows too many: up to
-// 32 rows the 32-row tiles, whose softmax is spread over all warps; well above 128
-// the 256-row ones, whose halves share every key tile.
+// 32 rows the 32-row tiles, whose softmax is spread over all warps, else the
+// 128-row ones.  16 sequences of 1024 keys, 8 kv heads: 16 rows 24.2 us the first way
+// and 29.3 the second, 32 rows 24.3 and 26.1; 40 rows, two tiles the first way, 31.9
+// and 27.1.
 int query_tiles(int n_rows, int items, int G) {
   const long long rows = (long long)std::max(n_rows / items, 1) * G;
-  return rows <= 32 ? kPagedQuad : rows > 144 ? kPagedPair : kPagedSplit;
+  return rows <= 32 ? kPagedQuad : kPagedSplit;
 }
 
-// Workspace: status word, launch epoch and announcements of parts (cleared once),
-// a record per CTA, the parts of cut query tiles.
-constexpr size_t kWsEpoch = 64, kWsReady = 256, kWsCut = 1024, kWsParts = 4096;
-static_assert(kWsReady + sizeof(int) * kNumSMs <= kWsCut, "the announcements fit");
+// Workspace: status word (cleared once), a record per CTA, the parts of cut query
+// tiles.
+constexpr size_t kWsCut = 256, kWsParts = 4096;
 static_assert(kWsCut + sizeof(int4) * kNumSMs <= kWsParts, "the records fit before the parts");
 
 int slot_rows(long long n_rows, int G) {
-  const long long rows = n_rows * G;
-  return rows > 128 ? 256 : (int)((rows + 7) / 8 * 8);
+  return (int)std::min((n_rows * G + 7) / 8 * 8, 128ll);
 }
 size_t workspace_bytes(const PagedPool& kv, int slot) {
   return kWsParts + (size_t)2 * kNumSMs * slot * (kv.D * sizeof(float) + sizeof(float2));
@@ -175,7 +175,7 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
   p.slot_rows = slot_rows(p.bt.n_rows, p.G);
   if (ws_bytes < workspace_bytes(p.kv, p.slot_rows)) return DLLM_ERR_WORKSPACE;
   const int mode = query_tiles(p.bt.n_rows, groups ? p.n_groups : p.bt.n_seqs, p.G);
-  p.slot_rows = std::min(p.slot_rows, mode == kPagedQuad ? 32 : mode == kPagedSplit ? 128 : 256);
+  if (mode == kPagedQuad) p.slot_rows = std::min(p.slot_rows, 32);
   const int D = p.kv.D;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.rows_per_tile = (mode == kPagedQuad ? 32 : 128) / p.G;
@@ -191,8 +191,6 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
   p.scale_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.f / sqrtf((float)D));
   p.lse = lse;
   p.status = static_cast<int*>(ws);
-  p.epoch = reinterpret_cast<int*>(w + kWsEpoch);
-  p.ready = reinterpret_cast<int*>(w + kWsReady);
   p.cut = reinterpret_cast<int4*>(w + kWsCut);
   p.part = reinterpret_cast<float*>(w + kWsParts);
   p.part_ml = reinterpret_cast<float2*>(p.part + (size_t)2 * kNumSMs * p.slot_rows * D);

@@ -420,8 +420,8 @@ dllm_status dllm_paged_append(const dllm_kv_pages* kv, const dllm_paged_batch* b
 dllm_status dllm_paged_workspace_size(const dllm_kv_pages* kv, int32_t n_q_heads,
                                       int32_t max_rows, size_t* bytes);
 
-/* Clear the workspace's status word and bookkeeping (256-byte aligned ws); once
- * per workspace, before the calls that use it.
+/* Clear the workspace's status word (256-byte aligned ws); once per workspace,
+ * before the calls that use it.
  * dllm_device_status reads the word.  A workspace serves one call at a time. */
 dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream stream);
 
