@@ -4,6 +4,8 @@
 #include <float.h>
 #include <limits.h>
 
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -282,7 +284,7 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 // 54.5 us, the same rate; blocks of 32 rows of 16 sequences, 32 heads, 278 MB: 60 us,
 // 4.7 TB/s; in the steady state 6 TB/s, the rest is the start and the merge); many
 // by the products and the softmax between them (32 blocks of 32 rows that share 8192
-// keys 140 us, 890 TFLOP/s; two chunks of 1024 rows at 2 to 4 thousand keys 90 us,
+// keys 135 us, 920 TFLOP/s; two chunks of 1024 rows at 2 to 4 thousand keys 90 us,
 // 630); short ones by latency (32 rows over 544 keys 14 us).
 //
 // All query tiles of all items and kv heads, each with its key tiles plus a
@@ -918,7 +920,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint64_t k_desc = smem_desc(smem_u32(k_s), 16, 8 * C::kRowBytes, C::kSw);
       const uint64_t v_desc = smem_desc(smem_u32(v_s), C::kBoxBytes, 8 * C::kRowBytes, C::kSw);
       int n_piece = 0, n_q = 0, n_tile = 0;
-      int n_p[2] = {0, 0};  // P tiles taken of each stream
+      int k_st = 0, v_st = 0;  // places in the rings, and the parities of their barriers
+      uint32_t k_ph = 0, v_ph = 0, p_ph = 0;  // (of P: a bit a stream)
       bool ok = true;
       while (ok) {
         const int qi = n_piece % kQueue;
@@ -929,36 +932,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ++n_piece;
         if (n < 0) break;
         if (n == 0) continue;
-        auto wait_k = [&](int j) {
-          const int ti = n_tile + j;
-          return warp_wait(&k_full[ti % STK], (ti / STK) & 1, abort);
-        };
-        auto wait_v = [&](int j) {
-          const int ti = n_tile + j;
-          return warp_wait(&v_full[ti % STV], (ti / STV) & 1, abort);
-        };
-        // S of key tile j in stream x; then K (and after the last tile Q) is free
-        auto s_mma = [&](int x, int j) {
-          const int st = (n_tile + j) % STK;
-          const uint64_t kd = k_desc + (uint64_t)(st * C::kTile >> 4);
-          if (elect_one()) {
+        // (one thread) S of the next key tile into stream x; then K, after the last tile
+        // Q, is free
+        auto s_steps = [&](int x, bool last) {
+          const uint64_t kd = k_desc + (uint64_t)(k_st * C::kTile >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              constexpr int kPerBox = C::kBoxD / 16;
-              const int off = (kk / kPerBox) * C::kBoxBytes + (kk % kPerBox) * 32;
-              umma_bf16(tmem + x * 128, q_desc + (off >> 4), kd + (off >> 4), kIdS, kk > 0);
-            }
-            umma_commit(&s_full[x]);
-            umma_commit(&k_empty[st]);
-            if (j == n - 1) umma_commit(q_empty);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            constexpr int kPerBox = C::kBoxD / 16;
+            const int off = (kk / kPerBox) * C::kBoxBytes + (kk % kPerBox) * 32;
+            umma_bf16(tmem + x * 128, q_desc + (off >> 4), kd + (off >> 4), kIdS, kk > 0);
           }
-          __syncwarp();
+          umma_commit(&s_full[x]);
+          umma_commit(&k_empty[k_st]);
+          if (last) umma_commit(q_empty);
         };
-        // O of stream x.  128-key rows have the second half of P ready first: where
-        // the whole is not there yet, its products start.
-        auto pv_mma = [&](int x, int j, bool accumulate) {
-          const int st = (n_tile + j) % STV;
-          const uint64_t vd = v_desc + (uint64_t)(st * C::kTile >> 4);
+        auto next_k = [&]() {
+          if (++k_st == STK) {
+            k_st = 0;
+            k_ph ^= 1;
+          }
+        };
+        // O of stream x with key tile j, then (MORE) S of tile j + 2.  128-key rows have
+        // the second half of P ready first: where the whole is not there yet, its
+        // products start, and K is waited for, so that the S follows P at once (32
+        // blocks 141 -> 135 us).  32-row tiles wait for K behind the product, since
+        // there the keys come late (16 sequences' blocks 60.4 the other way, 59.5).
+        auto turn = [&](int x, int j, auto more) {
+          constexpr bool MORE = decltype(more)::value;
+          const uint64_t vd = v_desc + (uint64_t)(v_st * C::kTile >> 4);
           constexpr int kSteps = kKeyTile / 16;
           auto steps = [&](int from, bool acc) {
 #pragma unroll
@@ -966,41 +967,56 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               umma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + (from + k) * 8,
                           vd + ((from + k) * 16 * C::kRowBytes >> 4), kIdO, acc || k > 0);
           };
-          const uint32_t parity = n_p[x]++ & 1;
+          const uint32_t parity = p_ph >> x & 1;
+          p_ph ^= 1u << x;
+          if (!warp_wait(&v_full[v_st], v_ph, abort)) return false;
           if constexpr (!QUAD) {
             if (!warp_wait(&p_half[x], parity, abort)) return false;
             tc_fence_after();
-            if (elect_one()) steps(kSteps / 2, accumulate);
+            if (elect_one()) steps(kSteps / 2, j > 1);
             __syncwarp();
           }
+          if (!QUAD && MORE && !warp_wait(&k_full[k_st], k_ph, abort)) return false;
           if (!warp_wait(&p_full[x], parity, abort)) return false;
           tc_fence_after();
           if (elect_one()) {
-            *progress = n_tile + j + 1;
-            if constexpr (QUAD) steps(kSteps / 2, accumulate);
+            if constexpr (QUAD) steps(kSteps / 2, j > 1);
             steps(0, true);
-            umma_commit(&v_empty[st]);
+            umma_commit(&v_empty[v_st]);
+            if constexpr (!QUAD && MORE) s_steps(x, j + 3 == n);
+            *progress = n_tile + j + 1;
           }
           __syncwarp();
+          if constexpr (QUAD && MORE) {
+            if (!warp_wait(&k_full[k_st], k_ph, abort)) return false;
+            if (elect_one()) s_steps(x, j + 3 == n);
+            __syncwarp();
+          }
+          if (++v_st == STV) {
+            v_st = 0;
+            v_ph ^= 1;
+          }
+          if constexpr (MORE) next_k();
           return true;
         };
         ok = warp_wait(q_full, n_q & 1, abort);
         if (!ok) break;
-        // Each turn takes P of a key tile, multiplies it, and issues the S after the
-        // next in its stream.  The streams take turns, from the one that the last
-        // piece did not end with.
+        // The streams take turns, from the one that the last piece did not end with.
         const int b = n_tile & 1;
 #pragma unroll 1
-        for (int j = -2; ok && j < n; ++j) {
-          const int x = (b + j) & 1;
-          if (j == 0) ok = n_q == 0 || warp_wait(o_empty, (n_q - 1) & 1, abort);
-          if (ok && j >= 0) ok = wait_v(j) && pv_mma(x, j, j > 1);
-          if (ok && j + 2 < n) {
-            ok = wait_k(j + 2);
-            tc_fence_after();
-            if (ok) s_mma(x, j + 2);
-          }
+        for (int j = 0; ok && j < min(n, 2); ++j) {
+          ok = warp_wait(&k_full[k_st], k_ph, abort);
+          tc_fence_after();
+          if (ok && elect_one()) s_steps((b + j) & 1, j + 1 == n);
+          __syncwarp();
+          next_k();
         }
+        if (ok) ok = n_q == 0 || warp_wait(o_empty, (n_q - 1) & 1, abort);
+        int j = 0;
+#pragma unroll 1
+        for (; ok && j + 2 < n; ++j) ok = turn((b + j) & 1, j, std::true_type());
+#pragma unroll 1
+        for (; ok && j < n; ++j) ok = turn((b + j) & 1, j, std::false_type());
         if (ok && elect_one()) umma_commit(o_full);
         __syncwarp();
         n_tile += n;
