@@ -280,8 +280,8 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 // input type demands), the sum takes it unrounded.
 //
 // What bounds it, measured: few query rows by the keys' bytes (a token each of 32
-// sequences, 28 heads over 4, 270 MB: 57 us, 4.9 TB/s; one token over 131,001 keys
-// 54.5 us, the same rate; blocks of 32 rows of 16 sequences, 32 heads, 278 MB: 60 us,
+// sequences, 28 heads over 4, 281 MB: 57 us, 4.9 TB/s; one token over 131,001 keys
+// 54.5 us, the same rate; blocks of 32 rows of 16 sequences, 32 heads, 284 MB: 60 us,
 // 4.7 TB/s; in the steady state 6 TB/s, the rest is the start and the merge); many
 // by the products and the softmax between them (32 blocks of 32 rows that share 8192
 // keys 135 us, 920 TFLOP/s; two chunks of 1024 rows at 2 to 4 thousand keys 90 us,
@@ -1445,7 +1445,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // where there are fewer items than warps, several warps share an item's parts.  The
 // parts of a tile are in the slot of the CTA it starts in and in the even slots of
 // the CTAs after it; they are added in that order.  Bound by latency: 4 to 5 us for
-// up to 38 MB of parts that are still in L2.  One resident wave of blocks: a grid
+// up to 19 MB of parts that are still in L2.  One resident wave of blocks: a grid
 // with blocks for every CTA that mostly find nothing took 2 to 5 us more.
 constexpr int kMergeWarps = 8, kMergeBlocks = 4 * kNumSMs;
 
