@@ -315,7 +315,7 @@ def test_attn_row_limits(case, mask):
 @pytest.mark.parametrize("case", [
     (BF, 128, 28, 4, 16, "heads", [1, 3, 2], whole(300, 129, 128)),       # 32-row tiles
     (HF, 128, 8, 8, 64, "slots", [40, 100, 33], whole(300, 700, 64)),      # 128-row tiles
-    (BF, 64, 8, 2, 256, "heads", [90, 300], whole(900, 400)),              # 256-row tiles
+    (BF, 64, 8, 2, 256, "heads", [90, 300], whole(900, 400)),              # several tiles
 ], ids=lambda c: str(c)[:60])
 def test_slots_beyond_all_limits_hold_anything(case):
     lens = [sg[0][1] for sg in case[7]]
