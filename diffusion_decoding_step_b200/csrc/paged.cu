@@ -1047,7 +1047,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const bool valid = rr < d.nrows;
       const bool active = __any_sync(0xffffffffu, valid);
       const int r = d.r0 + rr;
-      const int limit = valid && p.row_limit != nullptr ? p.row_limit[r] : INT_MAX;
+      // (below zero is as zero, and the differences with positions stay in range)
+      const int limit = valid && p.row_limit != nullptr ? max(p.row_limit[r], 0) : INT_MAX;
       float m = -FLT_MAX, l = 0.f;
       // take the new maximum over; O and the sum are rescaled when it grew a lot
       auto grow = [&](bool first, float m_new) {
