@@ -396,9 +396,12 @@ struct Shares {
   }
 };
 
+// A sum of zero is a row without keys; one that is not a number, of a query or key that
+// is not finite, stays one.
 DLLM_DEV float log_sum(float m, float l) {  // of a maximum in log2 units and a sum
-  return l > 0.f ? fmaf(0.6931471805599453f, m, logf(l)) : -INFINITY;
+  return l != 0.f ? fmaf(0.6931471805599453f, m, logf(l)) : -INFINITY;
 }
+DLLM_DEV float inverse_sum(float l) { return l != 0.f ? 1.f / l : 0.f; }
 
 // Transpose of N units of 16 bytes among N neighbouring lanes (N = 2 or 4): after it
 // unit i of a lane is unit (lane % N) of the i-th lane of the group.
@@ -1261,7 +1264,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           reinterpret_cast<float4*>(p.part) + (size_t)d.slot * p.slot_rows * (D / 4) + qrow;
       const bool whole = d.parts == 1;
       if (whole) {
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv = inverse_sum(lt);
         a0 *= inv;
         a1 *= inv;
       }
@@ -1337,7 +1340,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 *reinterpret_cast<uint4*>(out + col) = make_uint4(u[0], u[1], u[2], u[3]);
               else
                 *reinterpret_cast<uint2*>(out + col) = make_uint2(u[0], u[1]);
-            } else if (lt > 0.f) {
+            } else if (lt != 0.f) {
 #pragma unroll
               for (int i = 0; i < kOwn; i += 4)
                 part[(c0 + col + i) / 4 * p.slot_rows] =
@@ -1366,7 +1369,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (some0) add(at, a0);
           if (some1) add(at + 128, a1);
           if (!whole) {
-            if (valid && lt > 0.f) {
+            if (valid && lt != 0.f) {
 #pragma unroll
               for (int i = 0; i < kC; i += 4)
                 part[(c0 + c * kC + i) / 4 * p.slot_rows] =
@@ -1535,7 +1538,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
           sum.join(ml_s[warp + k][lane], o_s[warp + k][0][lane], o_s[warp + k][1][lane]);
     }
     if (have && wpart == 0) {
-      const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
+      const float inv = inverse_sum(sum.l);
       const int r = tile.x + rr, head = (tile.y >> 12) * p.G + hh;
       uint16_t* out =
           static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride + head * p.out.head_stride;

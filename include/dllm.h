@@ -434,7 +434,8 @@ dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream str
  * h / (n_q_heads / n_kv_heads); scores are scaled by `scale` (0: 1/sqrt(D)).
  * out[r][h] = softmax-weighted values; lse[r][h] (fp32 [n_rows][n_q_heads],
  * NULL: not wanted) = the natural log of the sum of exponentials.  A row that
- * sees nothing gets out = 0 and lse = -inf.  Slots that no row sees (outside
+ * sees nothing gets out = 0 and lse = -inf; one whose scores are not numbers
+ * gets NaN in both.  Slots that no row sees (outside
  * the segments, or beyond the limits of all rows) may hold anything, infinities
  * and NaN included; what some row sees must be finite, since rows that do not
  * see it are multiplied with it as well, at weight zero.  scale is at most
