@@ -327,6 +327,13 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //           costs each thread 32 exponentials instead of 128.  The eight partial
 //           results of a row are merged at the end of a piece.
 //
+// Values that are not finite.  A row's weight is zero for the keys that it does not
+// see, but zero times infinity is no number, and the product takes all keys for all
+// rows.  So in a key tile that some rows see and others do not (other sequences' rows,
+// earlier rows under a limit) the softmax looks through V while it is in shared memory.
+// What is not finite is set to zero there, and the rows that see it note the column and
+// the sign (both signs: NaN) and put it into their result at the end.
+//
 // A query tile that one CTA did alone is written out.  The parts of a cut tile
 // go to the workspace in fp32, and a second kernel merges them in the order of
 // the keys.
@@ -360,8 +367,9 @@ struct PagedCfg {
   // sequence
   static constexpr int kPlan = 4 * (kMaxSeqs + 4) * 4 + kMaxSeqs * 2;
   static constexpr int kX = 4096;  // (max, sum) of both streams, for two pieces
-  static constexpr size_t kSmem = 1024 + (1 + kSTK + kSTV) * kTile + kMerge + kPlan + kX +
-                                  kQueue * sizeof(Piece) + kTileQueue * 16 + 512;
+  static constexpr int kSpoil = 2 * 128 * (D / 32) * 8;  // column bits of both signs a row
+  static constexpr size_t kSmem = 1024 + (1 + kSTK + kSTV) * kTile + kMerge + kPlan + kX + kSpoil +
+                                  kQueue * sizeof(Piece) + kTileQueue * 16 + 640;
 };
 
 DLLM_DEV int key_tiles(int a, int e) {
@@ -454,6 +462,32 @@ struct Meeting {
   }
 };
 
+// Pairs of 16-bit elements of which one is not finite get its top bit set: the exponent
+// is all ones.
+template <bool F16>
+DLLM_DEV uint32_t not_finite(uint32_t u) {
+  constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u, kOne = F16 ? 0x04000400u : 0x00800080u;
+  return ((u & kExp) + kOne) & 0x80008000u;
+}
+// What column col of a row gets from the values it saw that were not finite: infinity,
+// NaN or nothing (zero), from its bits in n entries of 2 * W words, which are cleared.
+template <int W>
+DLLM_DEV float spoilt_by(uint32_t* bits, int first, int step, int n, int col) {
+  const uint32_t bit = 1u << (col & 31);
+  bool sign[2] = {false, false};
+#pragma unroll 1
+  for (int i = 0; i < n; ++i)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint32_t* b = bits + (first + i * step) * 2 * W + x * W + (col >> 5);
+      if (*b & bit) {
+        atomicAnd(b, ~bit);
+        sign[x] = true;
+      }
+    }
+  return sign[0] && sign[1] ? NAN : sign[0] ? INFINITY : sign[1] ? -INFINITY : 0.f;
+}
+
 // Sum over the block's threads before this one (all threads; scratch of one
 // entry per warp).
 DLLM_DEV int block_before(int v, int* scratch, int warp, int lane) {
@@ -496,9 +530,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   int* pk = gs + kMaxSeqs + 4;                               // [n_groups]
   short* gid = reinterpret_cast<short*>(pk + kMaxSeqs + 4);  // [n_seqs]
   float* x_s = reinterpret_cast<float*>(gid + kMaxSeqs);
-  Piece* queue = reinterpret_cast<Piece*>(x_s + C::kX / 4);
+  uint32_t* spoil_s = reinterpret_cast<uint32_t*>(x_s + C::kX / 4);  // [2][128][2 signs][D / 32]
+  Piece* queue = reinterpret_cast<Piece*>(x_s + C::kX / 4 + C::kSpoil / 4);
   int4* tiles_s = reinterpret_cast<int4*>(queue + kQueue);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(tiles_s + kTileQueue);  // [STK]
+  // whether a stream took notes there, by pieces in turn [4][2 streams]
+  int* spoilt_s = reinterpret_cast<int*>(tiles_s + kTileQueue);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(spoilt_s + 8);  // [STK]
   uint64_t* k_empty = k_full + STK;          // [STK]
   uint64_t* v_full = k_empty + STK;          // [STV]
   uint64_t* v_empty = v_full + STV;          // [STV]
@@ -549,12 +586,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     mbar_init(done, 11);
     *abort = 0;
     *progress = 0;
+    for (int i = 0; i < 8; ++i) spoilt_s[i] = 0;
     fence_barrier_init();
     prefetch_tmap(&qmap);
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
   }
   if (warp == 9) tmem_alloc(tmem_slot, 512);
+  for (int i = t; i < C::kSpoil / 16; i += kAttnThreads)
+    reinterpret_cast<uint4*>(spoil_s)[i] = make_uint4(0, 0, 0, 0);
   grid_dep_wait();
 
   // ---- the line: row starts and groups (made non-decreasing, whatever they
@@ -736,19 +776,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         sg = seq_segs(p, i);
         own_total = seg_tiles(sg);
       }
-      // the largest limit of the rows from a to b
-      auto rows_limit = [&](int a, int b) {
-        int lim = 0;
+      // largest and least limit of sequence lim_s in this query tile: a slot beyond the
+      // largest is treated like one outside the segments, and may hold anything
+      int lim = INT_MAX, lim_lo = INT_MAX, lim_s = s_first;
+      auto rows_limit = [&](int a, int b) {  // of the rows from a to b
+        int hi = 0, lo = INT_MAX;
 #pragma unroll 1
-        for (int r = a + lane; r < b; r += 32) lim = max(lim, p.row_limit[r]);
-        return __reduce_max_sync(0xffffffffu, lim);
+        for (int r = a + lane; r < b; r += 32) {
+          const int x = p.row_limit[r];
+          hi = max(hi, x);
+          lo = min(lo, x);
+        }
+        lim = __reduce_max_sync(0xffffffffu, hi);
+        lim_lo = __reduce_min_sync(0xffffffffu, lo);
       };
-      // limit of sequence lim_s in this query tile: a slot beyond it is treated like
-      // one outside the segments, and may hold anything
-      int lim = INT_MAX, lim_s = s_first;
       if (p.row_limit != nullptr && rs[s_first + 1] >= r0 + nrows) {
         // all rows of one sequence: its last tiles may be beyond every row's limit
-        lim = rows_limit(r0, r0 + nrows);
+        rows_limit(r0, r0 + nrows);
         Segs s0 = sg;
         if constexpr (GROUPS)
           s0 = Segs{__shfl_sync(0xffffffffu, sg.a0, 0), __shfl_sync(0xffffffffu, sg.e0, 0),
@@ -822,6 +866,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         int kb, kl, kh, w, page;
       };
       // key tile k of the list, and this lane's page of it (n_pages: nothing to read)
+      // c.w: its rows, from | to << 9; whether their limits count (own keys) << 18;
+      // whether some of the query tile's rows see keys of it that others do not << 19
       auto locate = [&](int k) {
         Loc c;
         Segs x = sg;
@@ -850,13 +896,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int from = max(rs[s] - r0, 0), to = min(rs[s + 1] - r0, nrows);
           c.w = from | to << 9 | 1 << 18;
           if (p.row_limit != nullptr && (s != lim_s || lim == INT_MAX)) {
-            lim = rows_limit(r0 + from, r0 + to);
+            rows_limit(r0 + from, r0 + to);
             lim_s = s;
           }
           own_lim = lim;
+          if (to - from < nrows) c.w |= 1 << 19;
         }
         key_tile(x, kk, c.kb, c.kl, c.kh);
         c.kh = min(c.kh, own_lim);
+        if ((c.w >> 18 & 1) && lim_lo < c.kh) c.w |= 1 << 19;
         c.page = p.kv.n_pages;
         const int at = c.kb + lane * page_keys;
         if (lane < page_boxes && at < c.kh && at + page_keys > c.kl) {
@@ -1079,7 +1127,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ok = warp_wait(&t_full[ti % kTileQueue], (ti / kTileQueue) & 1, abort);
         if (!ok) break;
         const int4 tl = tiles_s[ti % kTileQueue];  // base, lo, hi, rows
-        const bool own = tl.w >> 18;
+        const bool own = tl.w >> 18 & 1, mixed = tl.w >> 19;
         const bool member = valid && rr >= (tl.w & 511) && rr < ((tl.w >> 9) & 511);
         const int first_k = tl.y - tl.x;
         const int end_k = member ? min(tl.z, own ? limit : INT_MAX) - tl.x : 0;
@@ -1092,106 +1140,131 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tc_fence_after();
         // Slots of a loaded page outside the tile's range may hold anything,
         // infinities and NaN included: their weight is zero, their values have
-        // to be as well.  (S is complete, so the products before it are, and the
-        // V tile that had this place had landed: the wait is for this tile's.)
-        if (tl.y > tl.x || tl.z < tl.x + kKeyTile) {
+        // to be as well.  So do values that are not finite in a mixed tile.  A warp sees
+        // to 32 keys.  (S is complete, so the products before it are, and the V tile that
+        // had this place had landed: the wait is for this tile's.)  This comes after
+        // the first probabilities, since V lands later than K: 32 blocks behind one prefix
+        // 134.3 us, and 144.5 with it before the maximum.
+        const bool clean = tl.y > tl.x || tl.z < tl.x + kKeyTile || mixed;
+        auto clean_values = [&]() {
           const int key = tl.x + row;
           const int pg = key & ~(page_keys - 1);
-          ok = warp_wait(&v_full[ti % STV], (ti / STV) & 1, abort);
-          if (!ok) break;
+          constexpr int kUnits = C::kRowBytes / 16;
+          uint8_t* v_tile = v_s + (ti % STV) * C::kTile;
+          // unit c of box b of a key, where the swizzle has put it
+          auto unit = [&](int k, int b, int c) {
+            return reinterpret_cast<uint4*>(v_tile + b * C::kBoxBytes + k * C::kRowBytes +
+                                            (c ^ (k * C::kRowBytes >> 7 & (kUnits - 1))) * 16);
+          };
+          if (!warp_wait(&v_full[ti % STV], (ti / STV) & 1, abort)) return false;
           if ((key < tl.y || key >= tl.z) && pg < tl.z && pg + page_keys > tl.y) {
-            uint4* v = reinterpret_cast<uint4*>(v_s + (ti % STV) * C::kTile + row * C::kRowBytes);
 #pragma unroll
             for (int b = 0; b < C::kNBox; ++b)
 #pragma unroll 1
-              for (int c = 0; c < C::kRowBytes / 16; ++c)
-                v[b * (C::kBoxBytes / 16) + c] = make_uint4(0, 0, 0, 0);
+              for (int c = 0; c < kUnits; ++c) *unit(row, b, c) = make_uint4(0, 0, 0, 0);
+          }
+          uint32_t any = 0;
+          if (mixed) {
+#pragma unroll
+            for (int b = 0; b < C::kNBox; ++b)
+#pragma unroll
+              for (int c = 0; c < kUnits; ++c) {
+                const uint4 u = *unit(row, b, c);
+                any |= not_finite<F16>(u.x) | not_finite<F16>(u.y) | not_finite<F16>(u.z) |
+                       not_finite<F16>(u.w);
+              }
+          }
+          unsigned bad = __ballot_sync(0xffffffffu, any != 0);
+          if (bad != 0) {
+            constexpr int W = D / 32;
+            // the notes of the last piece have been read and cleared
+            if (n_q > 0 && !warp_wait(o_empty, (n_q - 1) & 1, abort)) return false;
+            if (lane == 0) spoilt_s[(n_q & 3) * 2 + wg] = 1;
+#pragma unroll 1
+            for (; bad != 0; bad &= bad - 1) {
+              const int k = (warp & 3) * 32 + __ffs(bad) - 1;
+#pragma unroll 1
+              for (int w = 0; w < W; ++w) {  // a lane a column
+                const int e = w * 32 + lane;
+                const uint32_t u = reinterpret_cast<const uint16_t*>(
+                    unit(k, e / C::kBoxD, e % C::kBoxD / 8))[e & 7];
+                const bool is = not_finite<F16>(u), nan = u & (F16 ? 0x3ffu : 0x7fu), minus = u >> 15;
+                const unsigned pos = __ballot_sync(0xffffffffu, is && (nan || !minus));
+                const unsigned neg = __ballot_sync(0xffffffffu, is && (nan || minus));
+#pragma unroll 1
+                for (int x = lane; x < (QUAD ? 32 : 128); x += 32) {  // the rows that see it
+                  const int xr = x / p.G;
+                  if (xr >= d.nrows || xr < (tl.w & 511) || xr >= (tl.w >> 9 & 511)) continue;
+                  if (own && p.row_limit != nullptr && p.row_limit[d.r0 + xr] <= tl.x + k) continue;
+                  uint32_t* note =
+                      spoil_s + (wg * 128 + (QUAD ? (warp & 3) * 32 : 0) + x) * 2 * W + w;
+                  if (pos != 0) atomicOr(note, pos);
+                  if (neg != 0) atomicOr(note + W, neg);
+                }
+                __syncwarp();
+              }
+            }
+            __syncwarp();
+            if (any != 0) {
+#pragma unroll 1
+              for (int e = 0; e < D; ++e) {
+                uint16_t* u =
+                    reinterpret_cast<uint16_t*>(unit(row, e / C::kBoxD, e % C::kBoxD / 8)) + (e & 7);
+                if (not_finite<F16>(*u)) *u = 0;
+              }
+            }
           }
           fence_proxy_async_smem();
-        }
-        if (!sees) {
-          if (active) {  // no row of this warp sees the tile
-            const float none[16] = {};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_st16(s_tm + c * 16, none);
-            tmem_st_wait();
-          }
-          if constexpr (!QUAD) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_half[wg]);
-          }
-        } else if constexpr (QUAD) {
-          const int q0 = (warp & 3) * 32;  // this warp's quarter of the keys
-          float s[32];
-          tmem_ld32(s_tm + q0, s);
-          tmem_ld_wait32(s);
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (q0 + i < first_k || q0 + i >= end_k) s[i] = -INFINITY;
-          }
-          float mx[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-          const float m_new =
-              fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
-          grow(j == j0, m_new);
-          float pk[16], ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float p0 = fast_exp2(fmaf(s[2 * i], p.scale_log2, -m));
-            const float p1 = fast_exp2(fmaf(s[2 * i + 1], p.scale_log2, -m));
-            ls[i & 3] += p0 + p1;
-            pk[i] = __uint_as_float(pack2<F16>(p0, p1));
-          }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          return true;
+        };
+        if (!sees && active) {  // no row of this warp sees the tile
           const float none[16] = {};
 #pragma unroll
-          for (int c = 1; c < 4; ++c) tmem_st16(s_tm + (((warp & 3) + c) & 3) * 16, none);
-          tmem_st16(s_tm + (warp & 3) * 16, pk);
+          for (int c = 0; c < 4; ++c) tmem_st16(s_tm + c * 16, none);
+        }
+        if constexpr (QUAD) {
+          const int q0 = (warp & 3) * 32;  // this warp's quarter of the keys
+          if (sees) {
+            float s[32];
+            tmem_ld32(s_tm + q0, s);
+            tmem_ld_wait32(s);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (q0 + i < first_k || q0 + i >= end_k) s[i] = -INFINITY;
+            }
+            float mx[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+            const float m_new =
+                fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
+            grow(j == j0, m_new);
+            float pk[16], ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float p0 = fast_exp2(fmaf(s[2 * i], p.scale_log2, -m));
+              const float p1 = fast_exp2(fmaf(s[2 * i + 1], p.scale_log2, -m));
+              ls[i & 3] += p0 + p1;
+              pk[i] = __uint_as_float(pack2<F16>(p0, p1));
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            const float none[16] = {};
+#pragma unroll
+            for (int c = 1; c < 4; ++c) tmem_st16(s_tm + (((warp & 3) + c) & 3) * 16, none);
+            tmem_st16(s_tm + (warp & 3) * 16, pk);
+          }
+          if (clean) {
+            ok = clean_values();
+            if (!ok) break;
+          }
           tmem_st_wait();
         } else {
           // Half of the row stays in registers between the maximum and the
           // probabilities, the other half is read again.
-          if (masked) {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float s[32];
-              tmem_ld32(s_tm + c * 32, s);
-              tmem_ld_wait32(s);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c * 32 + i < first_k || c * 32 + i >= end_k) s[i] = -INFINITY;
-              tmem_st32(s_tm + c * 32, reinterpret_cast<const uint32_t*>(s));
-            }
-            tmem_st_wait();
-          }
           constexpr int kH = kKeyTile / 2;
-          float sa[kH], sb[kH];
-          float mx[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
-          auto maxima = [&](const float (&x)[kH]) {
-#pragma unroll
-            for (int i = 0; i < kH; i += 2)
-              mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(x[i], x[i + 1]));
-          };
-          auto load_half = [&](int h, float (&x)[kH]) {
-            tmem_ld32(s_tm + h * kH, x);
-            tmem_ld32(s_tm + h * kH + 32, x + 32);
-          };
-          auto landed = [&](float (&x)[kH]) {
-            tmem_ld_wait32(x);
-            tmem_ld_wait32(x + 32);
-          };
-          load_half(0, sa);
-          landed(sa);
-          load_half(1, sb);
-          maxima(sa);
-          landed(sb);
-          maxima(sb);
-          grow(j == j0, fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2));
-          load_half(0, sa);
+          float sa[kH];
           F2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          uint32_t pk[32];
           // P of 64 keys in 32 columns.  (A share of the exponentials as polynomials
           // on the FMA pipe was slower: 161 us for the 32 blocks became 168, 172 and
           // 193 with two, three and four of eight.)
@@ -1204,18 +1277,61 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               pk[i / 2] = pack2<F16>(e.x, e.y);
             }
           };
-          uint32_t pk[32];
-          probs(sb, pk);
-          landed(sa);
-          tmem_st32(s_tm + 32, pk);
+          if (sees) {
+            if (masked) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                float s[32];
+                tmem_ld32(s_tm + c * 32, s);
+                tmem_ld_wait32(s);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (c * 32 + i < first_k || c * 32 + i >= end_k) s[i] = -INFINITY;
+                tmem_st32(s_tm + c * 32, reinterpret_cast<const uint32_t*>(s));
+              }
+              tmem_st_wait();
+            }
+            float sb[kH];
+            float mx[4] = {-FLT_MAX, -FLT_MAX, -FLT_MAX, -FLT_MAX};
+            auto maxima = [&](const float (&x)[kH]) {
+#pragma unroll
+              for (int i = 0; i < kH; i += 2)
+                mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(x[i], x[i + 1]));
+            };
+            auto load_half = [&](int h, float (&x)[kH]) {
+              tmem_ld32(s_tm + h * kH, x);
+              tmem_ld32(s_tm + h * kH + 32, x + 32);
+            };
+            auto landed = [&](float (&x)[kH]) {
+              tmem_ld_wait32(x);
+              tmem_ld_wait32(x + 32);
+            };
+            load_half(0, sa);
+            landed(sa);
+            load_half(1, sb);
+            maxima(sa);
+            landed(sb);
+            maxima(sb);
+            grow(j == j0, fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2));
+            load_half(0, sa);
+            probs(sb, pk);
+            landed(sa);
+            tmem_st32(s_tm + 32, pk);
+          }
+          if (clean) {
+            ok = clean_values();
+            if (!ok) break;
+          }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_half[wg]);
-          probs(sa, pk);
-          tmem_st32(s_tm, pk);
-          l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-          tmem_st_wait();
+          if (sees) {
+            probs(sa, pk);
+            tmem_st32(s_tm, pk);
+            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+            tmem_st_wait();
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -1228,11 +1344,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       n_tile += d.n;
       // ---- the piece's result
       float a0 = 1.f, a1 = 0.f, mt = m, lt = l;
+      int spoilt_all = 0;  // a bit for each stream that has notes
       if (d.n > 0) {  // (max, sum) of both streams; each takes half of the columns
         float2* x = reinterpret_cast<float2*>(x_s) + (n_q & 1) * 256;
         x[wg * 128 + row] = make_float2(m, l);
         ok = all.join(lane, abort);
         if (!ok) break;
+        spoilt_all = spoilt_s[(n_q & 3) * 2] | spoilt_s[(n_q & 3) * 2 + 1] << 1;
+        // for the next piece but one, which no warp starts before all met for the next
+        if ((t & 127) == 0) spoilt_s[((n_q + 2) & 3) * 2 + wg] = 0;
         const float2 y0 = x[row], y1 = x[128 + row];  // a stream without tiles has sum 0
         mt = fmaxf(y0.x, y1.x);
         if constexpr (QUAD) {
@@ -1270,6 +1390,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       uint16_t* out = static_cast<uint16_t*>(p.out.data) + r * p.out.row_stride +
                       head * p.out.head_stride + c0;
+      // over the row's columns from c on that values which are not finite go to
+      auto spoil = [&](int c, int n) {
+#pragma unroll 1
+        for (int col = c; col < c + n; ++col) {
+          float v = 0.f;
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x)
+            if (spoilt_all >> x & 1)
+              v += spoilt_by<D / 32>(spoil_s, x * 128 + (QUAD ? lane : row), 32, QUAD ? 4 : 1, col);
+          if (v == 0.f) continue;
+          if (whole)
+            out[col - c0] = (uint16_t)pack2<F16>(v, 0.f);
+          else if (lt != 0.f)
+            reinterpret_cast<float*>(part + col / 4 * p.slot_rows)[col & 3] = v;
+        }
+      };
       if constexpr (QUAD) {
         // each warp brings the sum of its streams for its quarter of the keys; the
         // four are added through shared memory, SW columns at a time, of which
@@ -1299,7 +1435,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               for (int i = 0; i < SW; ++i) v[i] = fmaf(w[i], a, v[i]);
             }
           }
-          if (c == kCols / SW - 1 && d.n > 0) {
+          if (c == kCols / SW - 1 && d.n > 0 && !spoilt_all) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_empty);
@@ -1346,6 +1482,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 part[(c0 + col + i) / 4 * p.slot_rows] =
                     make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
+            if (spoilt_all) spoil(c0 + col, kOwn);
           }
         }
       } else if (active) {
@@ -1398,7 +1535,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
       }
-      if (!QUAD && d.n > 0) {
+      if (!QUAD && spoilt_all) {
+        __syncwarp();
+        if (valid) spoil(c0, kCols);
+      }
+      if ((!QUAD && d.n > 0) || spoilt_all) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_empty);

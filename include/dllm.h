@@ -435,11 +435,11 @@ dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream str
  * out[r][h] = softmax-weighted values; lse[r][h] (fp32 [n_rows][n_q_heads],
  * NULL: not wanted) = the natural log of the sum of exponentials.  A row that
  * sees nothing gets out = 0 and lse = -inf; one whose scores are not numbers
- * gets NaN in both.  Slots that no row sees (outside
- * the segments, or beyond the limits of all rows) may hold anything, infinities
- * and NaN included; what some row sees must be finite, since rows that do not
- * see it are multiplied with it as well, at weight zero.  scale is at most
- * 2^127.
+ * gets NaN in both.  Slots that a row does not see (outside the segments,
+ * beyond its limit, or another sequence's) may hold anything, infinities and
+ * NaN included, and change nothing in its result; a value that is not finite
+ * and that it sees makes its column of the result infinite or NaN.  scale is
+ * at most 2^127.
  * out must not overlap q. */
 dllm_status dllm_paged_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
                             int32_t n_q_heads, const int32_t* segs, const int32_t* row_limit,

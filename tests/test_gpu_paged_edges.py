@@ -88,3 +88,137 @@ def test_rows_that_are_not_numbers_stay_so(case, grouped):
     if n > 1 and not grouped:
         assert (out[n - 1] == 0).all() and (lse[n - 1] == -math.inf).all()
     assert kv.device_status() == 0
+
+
+# ------------------------------------------------------------------ keys and values that are not finite
+def attention_of_marked(q, k, v, seen, hkv, dtype):
+    """One sequence: q [rows][Hq][D], k and v [keys][Hkv][D] in float64 that need not be finite,
+    seen [rows][keys].  Returns out, lse, their bounds as in paged_ref, and where out is not
+    finite: a score of NaN or plus infinity spoils its row and head, a value its column, in the
+    rows that see it; a score of minus infinity has weight zero."""
+    G, D = q.shape[1] // hkv, q.shape[2]
+    q = q.to(R.F64).reshape(len(q), hkv, G, D)
+    x = torch.einsum("rhgd,khd->rhgk", q, k) * D ** -0.5
+    x = torch.where(seen[:, None, None], x, -math.inf)
+    size = torch.einsum("rhgd,khd->rhgk", q.abs(), k.abs()) * D ** -0.5
+    B = torch.where(torch.isfinite(x), size, torch.zeros_like(size)).amax(3)
+    lost = (torch.isnan(x) | (x == math.inf)).any(3)
+    x = torch.where(lost[..., None], torch.zeros_like(x), x)
+    z = torch.logsumexp(x, 3)
+    w = torch.where(torch.isfinite(z)[..., None], torch.exp(x - z[..., None]), torch.zeros_like(x))
+    fine = torch.isfinite(v)
+    vf = torch.where(fine, v, torch.zeros_like(v))
+    o, A = torch.einsum("rhgk,khd->rhgd", w, vf), torch.einsum("rhgk,khd->rhgd", w, vf.abs())
+    spoilt = torch.einsum("rk,khd->rhd", seen.to(R.F64), (~fine).to(R.F64))[:, :, None] > 0
+    spoilt = spoilt | lost[..., None]
+    e = R.EPS[dtype]
+    shift = 2 * D * 2.0 ** -23 * B + 2.0 ** -16
+    sub = seen.sum(1)[:, None, None, None] * 2.0 ** -25 * vf.abs().amax() if dtype == HF else 0.0
+    tol = e / 2 * o.abs() + (e / 2 + shift[..., None]) * A * (1 + e) + sub + 2.0 ** -25
+    return [t.flatten(1, 2) for t in (o, z, tol, shift, spoilt, lost)]
+
+
+def run_spoilt(dtype, D, hq, hkv, ps, layout, rows, segs, bad, limit=None, groups=None, seed=0):
+    """bad: (sequence, position, "k" or "v", column, value): an element of one kv head of a
+    sequence's own keys or values.  Only the rows that see it may change."""
+    g = _gen(seed + D + sum(rows))
+    top = [max(a + n for a, n in sg) for sg in segs]
+    pre = groups[1] if groups else []
+    n_pages = sum(-(-n // ps) for n in top + pre) + 2
+    pool = make_pool(g, n_pages, hkv, ps, D, dtype, layout)
+    order = torch.randperm(n_pages, generator=g).to(torch.int32)
+    table, at = make_tables(top, ps, order)
+    ptable, _ = make_tables(pre, ps, order, at) if groups else (None, at)
+    n = sum(rows)
+    rs = [sum(rows[:i]) for i in range(len(rows) + 1)]
+    q = torch.randn(n, hq, D, generator=g).to(dtype).to(DEV)
+    lim = None if limit is None else [limit(s, j) for s in range(len(rows)) for j in range(rows[s])]
+    for s, p, what, col, value in bad:
+        pool[what == "v"][int(table[s, p // ps]), (p + col) % hkv, p % ps, col] = value
+    pages, ref = host(pool), []
+    for s in range(len(rows)):
+        if not rows[s]:
+            continue
+        own = R.seq_positions(segs[s], table.shape[1] * ps)
+        k, v = pages.gather(table[s], own)
+        seen = torch.ones(rows[s], len(own), dtype=torch.bool)
+        if lim is not None:
+            seen = own[None] < torch.tensor(lim[rs[s]:rs[s + 1]])[:, None]
+        if groups:
+            i = [i for i in range(len(pre)) if groups[0][i] <= s < groups[0][i + 1]][0]
+            pk, pv = pages.gather(ptable[i], torch.arange(pre[i]))
+            k, v = torch.cat([pk, k], 1), torch.cat([pv, v], 1)
+            seen = torch.cat([torch.ones(rows[s], pre[i], dtype=torch.bool), seen], 1)
+        ref.append(attention_of_marked(q[rs[s]:rs[s + 1]].cpu(), k.transpose(0, 1), v.transpose(0, 1), seen, hkv, dtype))
+    o, z, tol, ztol, spoilt, lost = (torch.cat(x) for x in zip(*ref))
+    kv = make_kv(pool, hq, n, len(pre))
+    out, lse = torch.full_like(q, 3.0), torch.full((n, hq), 5.0, device=DEV)
+    a = (q, ints(rs), table.to(DEV), ints(segs))
+    kw = dict(row_limit=None if lim is None else ints(lim), out=out, lse=lse)
+    for _ in range(2):      # the second call finds what the first one left in the workspace
+        if groups:
+            kv.shared_prefix_attn(*a, ints(groups[0]), ptable.to(DEV), ints(pre), **kw)
+        else:
+            kv.attn(*a, **kw)
+        got, got_lse = out.cpu().to(R.F64), lse.cpu().to(R.F64)
+        assert not torch.isfinite(got[spoilt]).any()
+        assert torch.isfinite(got[~spoilt]).all()
+        assert ((got - o).abs() <= tol)[~spoilt].all()
+        assert torch.isnan(got_lse[lost]).all()
+        none = torch.isinf(z) & ~lost
+        assert (got_lse[none] == -math.inf).all()
+        assert ((got_lse - z).abs() <= ztol)[~lost & ~none].all()
+    assert kv.device_status() == 0
+
+
+NAN, INF = math.nan, math.inf
+
+
+def every(s, n, D, step=1):
+    """All keys and values of a sequence's first n positions, in columns that differ."""
+    return [(s, p, what, (p * 5 + (what == "v")) % D, NAN if p % 3 else -INF) for p in range(0, n, step) for what in "kv"]
+
+
+SPOILT = [  # dtype, D, Hq, Hkv, page, layout, rows, own segments, bad places, (first sequences, prefix lengths)
+    (BF, 128, 28, 4, 16, "heads", [1, 1, 1], whole(1, 40, 300),
+     [(1, 5, "v", 3, NAN), (2, 299, "v", 127, INF), (2, 0, "v", 64, -INF)], ([0, 3], [500])),
+    (BF, 128, 28, 4, 16, "heads", [1, 1, 1], whole(40, 40, 300),
+     [(0, 39, "k", 3, NAN), (2, 150, "k", 100, INF), (2, 151, "v", 0, NAN)], ([0, 3], [70])),
+    (HF, 128, 32, 32, 64, "slots", [32, 7, 32], whole(32, 100, 64), [(1, 99, "v", 1, INF)] + every(2, 64, 128),
+     ([0, 3], [130])),
+    (HF, 64, 8, 2, 32, "paired", [5, 0, 70, 3, 9], whole(20, 0, 400, 33, 0),
+     [(0, 19, "v", 63, NAN), (2, 399, "v", 0, INF), (2, 130, "v", 33, INF), (3, 0, "k", 0, NAN)], ([0, 5], [77])),
+    (BF, 64, 4, 4, 16, "padded", [2, 2, 2], whole(200, 500, 3), every(1, 500, 64, 7), ([0, 3], [1])),
+    (HF, 32, 4, 4, 8, "padded", [8, 8, 8, 8], whole(8, 60, 8, 130), [(3, 129, "v", 31, NAN), (1, 7, "v", 0, -INF)],
+     ([0, 4], [257])),
+    (BF, 32, 6, 1, 8, "heads", [40, 30], whole(140, 60), every(0, 140, 32, 9), ([0, 2], [30])),
+    # own lists that are cut over many CTAs
+    (BF, 128, 7, 1, 128, "heads", [1, 1, 1], whole(9000, 300, 1),
+     [(0, 8999, "v", 7, NAN), (0, 4000, "v", 8, INF), (0, 3000, "v", 8, -INF)], ([0, 3], [1000])),
+    (HF, 64, 14, 2, 64, "slots", [20, 9], whole(300, 20000), [(1, p, "v", p % 64, INF) for p in range(0, 20000, 997)],
+     ([0, 2], [400])),
+]
+
+
+@pytest.mark.parametrize("case", SPOILT, ids=lambda c: str(c)[:60])
+def test_sequences_of_a_group_do_not_spoil_each_other(case):
+    run_spoilt(*case[:9], groups=case[9])
+
+
+@pytest.mark.parametrize("case", [
+    (BF, 128, 28, 4, 16, "heads", [1, 3, 4], whole(300, 129, 128)),         # 32-row tiles
+    (HF, 64, 8, 2, 64, "slots", [70, 133], whole(700, 390)),                # 128-row tiles
+    (BF, 32, 4, 4, 8, "padded", [30, 17], whole(300, 40)),
+    (HF, 128, 4, 1, 32, "paired", [33], [((200, 300), (10, 50))]),
+    (BF, 128, 4, 4, 64, "heads", [200, 70], whole(400, 5000)),
+], ids=lambda c: str(c)[:60])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_later_keys_do_not_spoil_earlier_rows(case, grouped):
+    """Under a causal limit a row is the same whatever the positions beyond its own hold."""
+    rows, end = case[6], [max(a + n for a, n in sg) for sg in case[7]]
+    D, bad = case[1], []
+    for s, m in enumerate(rows):
+        bad += [(s, end[s] - 1 - j, "kv"[(j + 1) % 2], (11 * j + s) % D, [NAN, INF, -INF][j % 3])
+                for j in range(0, m, max(1, m // 4)) if any(a <= end[s] - 1 - j < a + n for a, n in case[7][s])]
+    run_spoilt(*case, bad, limit=lambda s, j: end[s] - rows[s] + j + 1,
+               groups=([0, len(rows)], [150]) if grouped else None)
