@@ -119,6 +119,8 @@ SIGNATURES = {
     "dllm_layer_stack_plan": (C.c_int, [_CFG, _I, C.POINTER(C.c_int32)]),
     "dllm_attention_plan": (C.c_int, [_CFG, _I, C.POINTER(C.c_int32)]),
     "dllm_selftest_wait_timeout": (C.c_int, [_P, C.c_int32, _P]),
+    "dllm_selftest_paged_timeout": (C.c_int, [_KV, _BT, _I, _P, _ROWS, _ROWS, _P, C.c_size_t, _I, _I,
+                                              _P]),
     "dllm_status_string": (C.c_char_p, [C.c_int]),
 }
 

@@ -327,7 +327,12 @@ struct PagedAttnParams {
   float* part;
   float2* part_ml;
   int4* cut;
+  unsigned long long wait_ns;  // the watchdog's limit
+  int stall;                   // PagedStall
 };
+// What the self-test holds back, so that the waits for it run out: the description of a
+// piece, the end of its products, a warp's part in the streams' meeting.
+enum PagedStall : int { kStallNone, kStallPiece, kStallProducts, kStallMeeting };
 // Query tiles of 128 rows, of 32 rows (paged.cu says how they work).
 enum PagedMode : int { kPagedSplit, kPagedQuad };
 cudaError_t paged_attn_prepare();

@@ -308,7 +308,9 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 //   warp 11     is the watchdog: the waits of the others are unbounded until it finds
 //               that nothing was multiplied for two seconds, reports that and lets
 //               them go.  (A clock in every wait made the code a tenth longer, and a
-//               launch pays for its code, which it fetches anew.)
+//               launch pays for its code, which it fetches anew.)  In a launch that gives
+//               up it waits for the copies and products in flight.  (The producers
+//               waiting for their own at their end: 32 blocks 135 -> 138 us.)
 //   warps 0-3 and 4-7   softmax of two streams with their own S, P and O in
 //               TMEM, so that the products of one run during the softmax of the
 //               other.  A thread owns a query row; P overwrites S in TMEM as the
@@ -448,14 +450,25 @@ DLLM_DEV bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abor
   return __all_sync(0xffffffffu, ok);
 }
 
+// The wait for copies or products that were issued, in a block that gives up: until they
+// are done, or at most kSettleNs.
+constexpr unsigned long long kSettleNs = 100000000ull;  // 0.1 s
+DLLM_DEV void settle(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity) && global_ns() - t0 < kSettleNs) {
+  }
+  __syncwarp();
+}
+
 // Warps meet at a barrier that counts one arrival of each; false when the watchdog
 // gave up.  (At a hardware barrier they would wait for warps that have left.)
 struct Meeting {
   uint64_t* bar;
   uint32_t parity = 0;
-  DLLM_DEV bool join(int lane, const volatile int* abort) {
+  // (withhold: the self-test's warp that does not arrive)
+  DLLM_DEV bool join(int lane, const volatile int* abort, bool withhold = false) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
+    if (lane == 0 && !withhold) mbar_arrive(bar);
     const bool ok = warp_wait(bar, parity, abort);
     parity ^= 1;
     return ok;
@@ -551,9 +564,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   uint64_t* o_empty = o_full + 1;
   uint64_t* meet = o_empty + 1;  // both streams; each one
   uint64_t* done = meet + 3;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* settled = done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(settled + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* progress = abort + 1;
+  volatile int* issued_s = progress + 1;  // copies of K, V and Q, when their warps have left
 
   const int t = threadIdx.x, warp = uniform(t >> 5), lane = t & 31;
   const int tile_rows = p.rows_per_tile;
@@ -584,6 +599,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     mbar_init(&meet[1], 4);
     mbar_init(&meet[2], 4);
     mbar_init(done, 11);
+    mbar_init(settled, 1);
     *abort = 0;
     *progress = 0;
     for (int i = 0; i < 8; ++i) spoilt_s[i] = 0;
@@ -718,6 +734,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         hi = mid;
     }
     int n_piece = 0, n_q = 0, n_tile = 0;  // pieces, with keys; key tiles
+    int q_issued = 0, issued = 0;          // copies of Q, of key tiles
     uint8_t* ring = k_side ? k_s : v_s;
     uint64_t* full = k_side ? k_full : v_full;
     uint64_t* empty = k_side ? k_empty : v_empty;
@@ -837,7 +854,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (first == cta) cut = make_int4(r0, nrows | kvh << 12, d.parts, d.slot);  // (lane 0's)
           }
           queue[qi] = d;
-          mbar_arrive(&d_full[qi]);
+          if (p.stall != kStallPiece) mbar_arrive(&d_full[qi]);
         }
       }
       ++n_piece;
@@ -859,6 +876,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               tma_load_3d(q_s + h * 32 * C::kRowBytes + b * C::kBoxBytes, &qmap, q_full,
                           b * C::kBoxD, q_head, q_row);
         }
+        q_issued += ok;
       }
       ++n_q;
 
@@ -946,6 +964,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tiles_s[ti % kTileQueue] = make_int4(c.kb, c.kl, c.kh, c.w);
           mbar_arrive(&t_full[ti % kTileQueue]);
         }
+        ++issued;
         c = next;
       }
       n_tile += n;
@@ -961,6 +980,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         p.cut[cta] = cut;
       }
+    }
+    if (lane == 0) {
+      issued_s[k_side ? 0 : 1] = issued;
+      if (k_side) issued_s[2] = q_issued;
     }
   } else if (warp == 9) {
     // ================================================================ products
@@ -1068,11 +1091,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (; ok && j + 2 < n; ++j) ok = turn((b + j) & 1, j, std::true_type());
 #pragma unroll 1
         for (; ok && j < n; ++j) ok = turn((b + j) & 1, j, std::false_type());
-        if (ok && elect_one()) umma_commit(o_full);
+        if (ok && p.stall != kStallProducts && elect_one()) umma_commit(o_full);
         __syncwarp();
         n_tile += n;
         ++n_q;
       }
+      if (elect_one()) umma_commit(settled);
     }
   } else if (warp < 8) {
     // ================================================================ softmax
@@ -1348,7 +1372,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (d.n > 0) {  // (max, sum) of both streams; each takes half of the columns
         float2* x = reinterpret_cast<float2*>(x_s) + (n_q & 1) * 256;
         x[wg * 128 + row] = make_float2(m, l);
-        ok = all.join(lane, abort);
+        ok = all.join(lane, abort, p.stall == kStallMeeting && warp == 0);
         if (!ok) break;
         spoilt_all = spoilt_s[(n_q & 3) * 2] | spoilt_s[(n_q & 3) * 2 + 1] << 1;
         // for the next piece but one, which no warp starts before all met for the next
@@ -1551,6 +1575,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           p.lse[(size_t)r * p.Hq + head] = log_sum(mt, lt);
       }
     }
+    tmem_st_wait();
   }
   if (warp == 11) {
     // ================================================================ watchdog
@@ -1561,16 +1586,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (now != seen) {
         seen = now;
         t0 = global_ns();
-      } else if (!*abort && global_ns() - t0 > kWaitLimitNs) {
+      } else if (!*abort && global_ns() - t0 > p.wait_ns) {
         *abort = 1;
         if (lane == 0 && p.status != nullptr) atomicOr(p.status, kErrTimeout);
       }
     }
-  } else {
     if (*abort) {  // copies and products in flight end before the block goes
-      const unsigned long long t0 = global_ns();
-      while (global_ns() - t0 < 100000ull) __nanosleep(1000);
+      for (int k = max(issued_s[0] - STK, 0); k < issued_s[0]; ++k)
+        settle(&k_full[k % STK], (k / STK) & 1);
+      for (int k = max(issued_s[1] - STV, 0); k < issued_s[1]; ++k)
+        settle(&v_full[k % STV], (k / STV) & 1);
+      if (issued_s[2] > 0) settle(q_full, (issued_s[2] - 1) & 1);
+      settle(settled, 0);
     }
+  } else {
     __syncwarp();
     if (lane == 0) mbar_arrive(done);
   }

@@ -11,6 +11,7 @@
 
 #include "../../include/dllm.h"
 #include "kernels.cuh"
+#include "ptx.cuh"
 
 namespace dllm {
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
@@ -141,8 +142,11 @@ dllm_status run_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
                      const dllm_prefix_groups* groups, int32_t n_q_heads, const int32_t* segs,
                      const int32_t* row_limit, float scale, const dllm_rows* q,
                      const dllm_rows* out, float* lse, void* ws, size_t ws_bytes,
-                     dllm_stream stream) {
+                     dllm_stream stream, int stall = kStallNone,
+                     unsigned long long wait_ns = kWaitLimitNs) {
   PagedAttnParams p{};
+  p.stall = stall;
+  p.wait_ns = wait_ns;
   dllm_status e = check_pool(kv, &p.kv);
   if (e == DLLM_OK) e = check_batch(batch, p.kv, &p.bt);
   if (e == DLLM_OK) e = check_heads(n_q_heads, p.kv);
@@ -292,6 +296,16 @@ dllm_status dllm_shared_prefix_attn(const dllm_kv_pages* kv, const dllm_paged_ba
   if (!groups) return DLLM_ERR_INVALID;
   return run_attn(kv, batch, groups, n_q_heads, segs, row_limit, scale, q, out, lse, ws, ws_bytes,
                   stream);
+}
+
+dllm_status dllm_selftest_paged_timeout(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
+                                        int32_t n_q_heads, const int32_t* segs,
+                                        const dllm_rows* q, const dllm_rows* out, void* ws,
+                                        size_t ws_bytes, int32_t where, int32_t limit_us,
+                                        dllm_stream stream) {
+  if (where < 0 || where > 2 || limit_us < 1 || limit_us > 1000000) return DLLM_ERR_INVALID;
+  return run_attn(kv, batch, nullptr, n_q_heads, segs, nullptr, 0.f, q, out, nullptr, ws, ws_bytes,
+                  stream, kStallPiece + where, 1000ull * limit_us);
 }
 
 }  // extern "C"

@@ -144,7 +144,9 @@ class PagedKV:
         return out
 
     def device_status(self) -> int:
-        """The workspace's status word (waits for the current stream)."""
+        """The workspace's status word (waits for the current stream): 0, or the DLLM_DEVICE_*
+        bits of all calls so far.  No call reads it: after DLLM_DEVICE_TIMEOUT outputs are
+        undefined, after DLLM_DEVICE_INDEX bad pages and positions were left out."""
         code = C.c_int32(0)
         with torch.cuda.device(self.device):
             stream = torch.cuda.current_stream(self.device).cuda_stream

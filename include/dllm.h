@@ -440,6 +440,8 @@ dllm_status dllm_paged_workspace_init(void* ws, size_t ws_bytes, dllm_stream str
  * NaN included, and change nothing in its result; a value that is not finite
  * and that it sees makes its column of the result infinite or NaN.  scale is
  * at most 2^127.
+ * A call whose waits run out (2 s without a product) sets DLLM_DEVICE_TIMEOUT
+ * in the workspace's status word and leaves out and lse undefined.
  * out must not overlap q. */
 dllm_status dllm_paged_attn(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
                             int32_t n_q_heads, const int32_t* segs, const int32_t* row_limit,
@@ -545,6 +547,17 @@ dllm_status dllm_attention_plan(const dllm_config* cfg, int32_t block_start, int
  * context stays usable afterwards. */
 #define DLLM_DEVICE_TIMEOUT 1
 dllm_status dllm_selftest_wait_timeout(int32_t* status, int32_t limit_us, dllm_stream stream);
+
+/* The same for dllm_paged_attn: a call whose waits run out after limit_us (1 to
+ * 1000000), because something in each working block is held back: the
+ * description of its work (where 0), the end of its products (1), a warp at the
+ * meeting of the softmax warps (2).  The call sets DLLM_DEVICE_TIMEOUT in ws,
+ * leaves out undefined and returns. */
+dllm_status dllm_selftest_paged_timeout(const dllm_kv_pages* kv, const dllm_paged_batch* batch,
+                                        int32_t n_q_heads, const int32_t* segs,
+                                        const dllm_rows* q, const dllm_rows* out, void* ws,
+                                        size_t ws_bytes, int32_t where, int32_t limit_us,
+                                        dllm_stream stream);
 
 const char* dllm_status_string(dllm_status s);
 

@@ -222,3 +222,72 @@ def test_later_keys_do_not_spoil_earlier_rows(case, grouped):
                 for j in range(0, m, max(1, m // 4)) if any(a <= end[s] - 1 - j < a + n for a, n in case[7][s])]
     run_spoilt(*case, bad, limit=lambda s, j: end[s] - rows[s] + j + 1,
                groups=([0, len(rows)], [150]) if grouped else None)
+
+
+# ------------------------------------------------------------------ waits that run out
+def c_call(pool, q, out, rs, table):
+    """Argument blocks of the C calls over these tensors."""
+    import ctypes as C
+
+    from diffusion_decoding_step_b200 import abi
+    k, v = pool
+    kv = abi.dllm_kv_pages(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), k.shape[0], k.shape[2],
+                           k.shape[1], k.shape[3], int(k.dtype is HF))
+    bt = abi.dllm_paged_batch(len(rs) - 1, q.shape[0], table.shape[1], table.stride(0), rs.data_ptr(), table.data_ptr())
+    rows = [abi.dllm_rows(x.data_ptr(), x.stride(0), x.stride(1)) for x in (q, out)]
+    return [C.byref(x) for x in (kv, bt, *rows)]
+
+
+@pytest.mark.parametrize("where", [0, 1, 2])
+@pytest.mark.parametrize("case", [
+    (BF, 128, 28, 4, 16, [1], [40000]),         # 32-row tiles, cut over all CTAs
+    (HF, 64, 8, 2, 64, [70, 133], [700, 390]),  # 128-row tiles
+    (BF, 32, 4, 1, 8, [1], [5]),                # one working CTA
+], ids=lambda c: str(c)[:60])
+def test_waits_that_run_out_are_reported(case, where):
+    """Something is held back in each working block, with a limit of 20 ms: the call reports it
+    and returns, and the next calls, this kernel's on the same workspace among them, are right."""
+    import ctypes as C
+    import time
+
+    from diffusion_decoding_step_b200 import abi
+    from tests.gpu_util import ptr, stream
+    dtype, D, hq, hkv, ps, rows, lens = case
+    g = _gen(5)
+    n_pages = sum(-(-n // ps) for n in lens) + 1
+    pool = make_pool(g, n_pages, hkv, ps, D, dtype, "heads")
+    table, _ = make_tables(lens, ps, torch.randperm(n_pages, generator=g).to(torch.int32))
+    n, rs = sum(rows), [sum(rows[:i]) for i in range(len(rows) + 1)]
+    q = torch.randn(n, hq, D, generator=g).to(dtype).to(DEV)
+    out, segs, r, t = torch.zeros_like(q), ints(whole(*lens)), ints(rs), table.to(DEV)
+    kv = make_kv(pool, hq, n)
+    want = kv.attn(q, r, t, segs)
+    a, b, qr, orow = c_call(pool, q, out, r, t)
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    abi.check(abi.dllm_selftest_paged_timeout(a, b, hq, ptr(segs), qr, orow, ptr(kv.ws), kv.ws.numel(), where, 20000,
+                                              stream()), "selftest")
+    torch.cuda.synchronize()
+    assert 0.015 <= time.perf_counter() - t0 < 5.0
+    assert kv.device_status() == abi.DLLM_DEVICE_TIMEOUT
+    abi.check(abi.dllm_paged_workspace_init(ptr(kv.ws), kv.ws.numel(), stream()), "init")
+    assert torch.equal(kv.attn(q, r, t, segs), want)
+    assert kv.device_status() == 0
+    check_rows(want, R.attention(host(pool), q.cpu(), rs, table, whole(*lens), dtype=dtype))
+
+
+def test_the_timeout_selftest_checks_its_arguments():
+    from diffusion_decoding_step_b200 import abi
+    from tests.gpu_util import ptr, stream
+    g = _gen(6)
+    pool = make_pool(g, 2, 1, 16, 64, BF, "heads")
+    kv = make_kv(pool, 1, 1)
+    q = torch.zeros(1, 1, 64, dtype=BF, device=DEV)
+    out, r, t, segs = torch.zeros_like(q), ints([0, 1]), ints([[0]]), ints(whole(3))
+    a, b, qr, orow = c_call(pool, q, out, r, t)
+    for where, limit in ((-1, 20), (3, 20), (0, 0), (0, 1000001)):
+        assert abi.dllm_selftest_paged_timeout(a, b, 1, ptr(segs), qr, orow, ptr(kv.ws), kv.ws.numel(), where, limit,
+                                               stream()) == abi.DLLM_ERR_INVALID
+    assert abi.dllm_selftest_paged_timeout(None, b, 1, ptr(segs), qr, orow, ptr(kv.ws), kv.ws.numel(), 0, 20,
+                                           stream()) == abi.DLLM_ERR_INVALID
+    assert kv.device_status() == 0
