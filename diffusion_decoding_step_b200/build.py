@@ -36,49 +36,64 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile the torch binding of the paged cache calls into _paged_torch.so."""
-    src = os.path.join(CSRC, "paged_torch.cpp")
-    deps = [src, os.path.join(HERE, "..", "include", "dllm.h")]
-    if not force and os.path.exists(BINDING) \
-            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
-        return BINDING
+def build_binding(force: bool = False) -> str | None:
+    """Compile the torch binding of the paged cache calls into _paged_torch.so; rebuilt
+    when its sources, torch or Python are others than it was built with.  Without torch or
+    Python's headers there is none: says so and returns None."""
     import sysconfig
 
-    import torch
+    src = os.path.join(CSRC, "paged_torch.cpp")
+    include = sysconfig.get_paths()["include"]
+    try:
+        import torch
+    except ImportError as e:
+        print(f"build: no torch ({e}): {os.path.basename(BINDING)} is left out", file=sys.stderr)
+        return None
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        print(f"build: no Python.h in {include}: {os.path.basename(BINDING)} is left out",
+              file=sys.stderr)
+        return None
+    made_for = f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+    stamp = BINDING + ".made_for"
+    deps = [src, os.path.join(HERE, "..", "include", "dllm.h")]
+    if not force and os.path.exists(BINDING) and os.path.exists(stamp) \
+            and open(stamp).read() == made_for \
+            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return BINDING
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = BINDING + ".tmp"
     subprocess.run(
         [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-         "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(root, "include"),
+         "-I" + include, "-I" + os.path.join(root, "include"),
          "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
          "-I" + os.path.join(cuda, "include"), src, "-o", tmp,
          "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
          "-lc10_cuda"], check=True)
     os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile every CUDA source into libdllm.so next to this file (with
-    debug=True: libdllm_debug.so, the DLLM_DEBUG build), and the torch binding."""
+    debug=True: libdllm_debug.so, the DLLM_DEBUG build), then the torch binding."""
     lib = LIB_DEBUG if debug else LIB
+    if force or stale(lib):
+        cmd = [nvcc(), *FLAGS]
+        if debug:
+            cmd += ["-DDLLM_DEBUG"]
+        if verbose:
+            cmd += ["-Xptxas", "-v"]
+        cmd += [os.path.join(CSRC, f) for f in SOURCES]
+        tmp = lib + ".tmp"
+        cmd += ["-o", tmp]
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, lib)
     if not debug:
         build_binding(force)
-    if not force and not stale(lib):
-        return lib
-    cmd = [nvcc(), *FLAGS]
-    if debug:
-        cmd += ["-DDLLM_DEBUG"]
-    if verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += [os.path.join(CSRC, f) for f in SOURCES]
-    tmp = lib + ".tmp"
-    cmd += ["-o", tmp]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, lib)
     return lib
 
 
