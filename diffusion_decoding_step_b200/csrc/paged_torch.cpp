@@ -212,9 +212,12 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor *gt = tensor(a[9], "group_start"), *pt = gt ? tensor(a[10], "prefix_table") : gt;
   if (!pt) return nullptr;
   const int64_t groups = gt->numel() - 1, width = pt->dim() == 2 ? pt->size(1) : -1;
-  if (groups < 1 || groups > h->max_groups || width > INT32_MAX)
-    return PyErr_Format(PyExc_ValueError, "%lld prefix groups: this PagedKV was made for 1 to %d",
+  if (h->max_groups < 1)
+    return PyErr_Format(PyExc_ValueError, "this PagedKV was made without prefix groups");
+  if (groups > h->max_groups || width > INT32_MAX)
+    return PyErr_Format(PyExc_ValueError, "%lld prefix groups: this PagedKV was made for up to %d",
                         (long long)groups, h->max_groups);
+  if (groups < 1) return PyErr_Format(PyExc_ValueError, "group_start: no prefix groups");
   dllm_prefix_groups g{(int32_t)groups, (int32_t)width, (int32_t)width, nullptr, nullptr, nullptr};
   if (!ints(*h, a[9], "group_start", {groups + 1}, &g.seq_start) ||
       !ints(*h, a[10], "prefix_table", {groups, -1}, &g.page_table) ||

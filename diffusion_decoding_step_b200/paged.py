@@ -33,7 +33,8 @@ class PagedKV:
     ``k_pages`` / ``v_pages``: bf16 or fp16 [n_pages][Hkv][page_size][D] on one GPU, with
     equal strides and contiguous D elements; other orders (slots before heads, keys and
     values of a page side by side) are views.  ``max_rows`` bounds the rows of an attention
-    call, ``max_groups`` the prefix groups (0: ``shared_prefix_attn`` is not used).
+    call and sizes the workspace; ``max_groups`` bounds the prefix groups (0: no
+    ``shared_prefix_attn``; the default is the most that a call takes).
 
     Calls run on the current stream of the pages' device and return without waiting.  The
     attention calls share one workspace: a PagedKV serves one of them at a time, and graphs or
@@ -42,7 +43,7 @@ class PagedKV:
     """
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, n_q_heads: int,
-                 max_rows: int, max_groups: int = 0):
+                 max_rows: int, max_groups: int = 1024):
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape \
                 or k_pages.stride() != v_pages.stride() or k_pages.dtype != v_pages.dtype \
                 or k_pages.device != v_pages.device:

@@ -291,3 +291,37 @@ def test_the_timeout_selftest_checks_its_arguments():
     assert abi.dllm_selftest_paged_timeout(None, b, 1, ptr(segs), qr, orow, ptr(kv.ws), kv.ws.numel(), 0, 20,
                                            stream()) == abi.DLLM_ERR_INVALID
     assert kv.device_status() == 0
+
+
+# ------------------------------------------------------------------ what PagedKV takes
+def small(groups=None, **kw):
+    """A PagedKV over four pages and the arguments of an attention call of three rows."""
+    from diffusion_decoding_step_b200.paged import PagedKV
+    g = _gen(24)
+    pool = make_pool(g, 4, 2, 16, 64, BF, "heads")
+    kv = PagedKV(pool[0], pool[1], 4, 3) if groups is None else PagedKV(pool[0], pool[1], 4, 3, groups)
+    q = torch.randn(3, 4, 64, generator=g).to(BF).to(DEV)
+    return pool, kv, q, (ints([0, 1, 3]), ints([[0, 1], [2, 0]]), ints(whole(20, 7)))
+
+
+def test_prefix_groups_need_no_announcement():
+    pool, kv, q, a = small()
+    pt, n = torch.tensor([[3], [1]], dtype=torch.int32), [9, 16]
+    out = kv.shared_prefix_attn(q, *a, ints([0, 1, 2]), pt.to(DEV), ints(n))
+    check_rows(out, R.attention(host(pool), q.cpu(), [0, 1, 3], a[1].cpu(), whole(20, 7), groups=([0, 1, 2], pt, n)))
+    assert kv.device_status() == 0
+
+
+def test_announced_prefix_groups_are_the_most():
+    _, kv, q, a = small(1)
+    g2 = (ints([0, 1, 2]), ints([[3], [1]]), ints([9, 16]))
+    with pytest.raises(ValueError, match="2 prefix groups.* 1"):
+        kv.shared_prefix_attn(q, *a, *g2)
+    _, kv, q, a = small(0)
+    with pytest.raises(ValueError, match="without prefix groups"):
+        kv.shared_prefix_attn(q, *a, *g2)
+    with pytest.raises(ValueError, match="without prefix groups"):
+        kv.shared_prefix_attn(q, *a, ints([0]), g2[1][:0], g2[2][:0])
+    _, kv, q, a = small()
+    with pytest.raises(ValueError, match="group_start"):
+        kv.shared_prefix_attn(q, *a, ints([0]), g2[1][:0], g2[2][:0])
