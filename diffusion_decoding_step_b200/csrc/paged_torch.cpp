@@ -108,9 +108,11 @@ bool batch(const Handle& h, PyObject* row_start, PyObject* table, int64_t n_rows
          ints(h, table, "page_table", {n, -1}, &out->page_table);
 }
 
+// A call without rows has nothing to do; the C ABI has no such calls.
 template <class F>
-PyObject* call(const Handle& h, F&& f) {
+PyObject* call(const Handle& h, int64_t n_rows, F&& f) {
   dllm_status status = DLLM_OK;
+  if (n_rows == 0) return PyLong_FromLong(status);
   std::string failed;
   Py_BEGIN_ALLOW_THREADS;
   try {  // no exception may pass the restoring of the thread's state
@@ -173,7 +175,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double theta = PyFloat_AsDouble(a[8]);
   if (theta == -1.0 && PyErr_Occurred()) return nullptr;
   if (given(a[9]) && !ints(*h, a[9], "rope_shift", {bt.n_seqs}, &shift)) return nullptr;
-  return call(*h, [&](dllm_stream s) {
+  return call(*h, n_rows, [&](dllm_stream s) {
     return h->append(&h->kv, &bt, has_q ? h->n_q_heads : 0, has_q ? &q : nullptr, &k, &v,
                      has_q ? &qo : nullptr, pos, shift, (float)theta,
                      static_cast<int32_t*>(h->ws), s);
@@ -205,7 +207,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (scale == -1.0 && PyErr_Occurred()) return nullptr;
   float* lp = static_cast<float*>(const_cast<void*>(lse));
   if (!given(a[9]))
-    return call(*h, [&](dllm_stream s) {
+    return call(*h, n_rows, [&](dllm_stream s) {
       return h->attn(&h->kv, &bt, h->n_q_heads, segs, limit, (float)scale, &q, &out, lp, h->ws,
                      h->ws_bytes, s);
     });
@@ -223,7 +225,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !ints(*h, a[10], "prefix_table", {groups, -1}, &g.page_table) ||
       !ints(*h, a[11], "prefix_len", {groups}, &g.len))
     return nullptr;
-  return call(*h, [&](dllm_stream s) {
+  return call(*h, n_rows, [&](dllm_stream s) {
     return h->shared(&h->kv, &bt, &g, h->n_q_heads, segs, limit, (float)scale, &q, &out, lp, h->ws,
                      h->ws_bytes, s);
   });

@@ -36,7 +36,8 @@ class PagedKV:
     call and sizes the workspace; ``max_groups`` bounds the prefix groups (0: no
     ``shared_prefix_attn``; the default is the most that a call takes).
 
-    Calls run on the current stream of the pages' device and return without waiting.  The
+    Calls run on the current stream of the pages' device and return without waiting; a call
+    without rows checks its arguments and does nothing.  The
     attention calls share one workspace: a PagedKV serves one of them at a time, and graphs or
     streams that may overlap each take a PagedKV of their own over the same pages.  Keep the
     object until its calls have run: the workspace's memory goes with it.

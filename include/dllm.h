@@ -343,7 +343,8 @@ dllm_status dllm_decode_all(const dllm_config* cfg, const dllm_weights* w, const
  * Rows.  A batch has n_seqs sequences; rows [row_start[s], row_start[s+1]) of
  * the row buffers belong to sequence s (any number, none included; row_start
  * is non-decreasing).  Rows before row_start[0] and behind row_start[n_seqs]
- * (a padded batch) are neither read for a result nor written.
+ * (a padded batch) are neither read for a result nor written.  A call has at
+ * least one sequence and n_rows of at least one.
  *
  * Pages.  Position p of sequence s lives in slot p % page_size of page
  * page_table[s*table_stride + p / page_size].  Sequences may share pages.

@@ -325,3 +325,27 @@ def test_announced_prefix_groups_are_the_most():
     _, kv, q, a = small()
     with pytest.raises(ValueError, match="group_start"):
         kv.shared_prefix_attn(q, *a, ints([0]), g2[1][:0], g2[2][:0])
+
+
+def test_a_call_without_rows_does_nothing():
+    pool, kv, q, a = small()
+    start = [x.clone() for x in pool]
+    k = torch.zeros(0, 2, 64, dtype=BF, device=DEV)
+    rs, rs0 = ints([0, 0, 0]), ints([0])
+    launched = None
+    from diffusion_decoding_step_b200 import abi
+    torch.cuda.synchronize()
+    launched = abi.dllm_launch_count()
+    for r, tab, segs, pos in ((rs, a[1], a[2], ints([5, 3])), (rs0, a[1][:0], a[2][:0], ints([]))):
+        assert kv.attn(q[:0], r, tab, segs).shape == (0, 4, 64)
+        assert kv.attn(q[:0], r, tab, segs, row_limit=ints([]), out=q[:0], lse=torch.zeros(0, 4, device=DEV)) is not None
+        assert kv.shared_prefix_attn(q[:0], r, tab, segs, ints([0, 0]), ints([[3]]), ints([9])).shape == (0, 4, 64)
+        assert kv.append(k, k, r, tab, pos, q=q[:0], rope_theta=1e4).shape == (0, 4, 64)
+        assert kv.append(k, k, r, tab, pos) is None
+    assert abi.dllm_launch_count() == launched
+    assert all(torch.equal(x, y) for x, y in zip(pool, start)) and kv.device_status() == 0
+    # the arguments are checked all the same
+    for f in (lambda: kv.attn(q[:0], rs, a[1], a[2][:1]), lambda: kv.append(k, k.half(), rs, a[1], ints([0, 0])),
+              lambda: kv.attn(q[:0], rs, a[1], a[2], row_limit=ints([1]))):
+        with pytest.raises(ValueError):
+            f()
