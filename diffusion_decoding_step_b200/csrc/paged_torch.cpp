@@ -130,6 +130,17 @@ PyObject* call(const Handle& h, int64_t n_rows, F&& f) {
 
 bool given(PyObject* o) { return o != Py_None; }
 
+// A number for the C ABI, which takes fp32, where zero stands for the default: one that
+// rounds to zero is refused.
+bool number(PyObject* o, const char* what, float* out) {
+  const double x = PyFloat_AsDouble(o);
+  if (x == -1.0 && PyErr_Occurred()) return false;
+  *out = (float)x;
+  if (x == 0.0 || *out != 0.f) return true;
+  PyErr_Format(PyExc_ValueError, "%s: %S is zero in 32 bits, which stands for the default", what, o);
+  return false;
+}
+
 // create(pages struct address, n_q_heads, max_rows, max_groups, device, is_f16, ws, ws_bytes,
 //        append, attn, shared)
 PyObject* create(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -172,12 +183,12 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (has_q && (!rows(*h, a[6], "q", n_rows, h->n_q_heads, &q) ||
                 !rows(*h, a[7], "q_out", n_rows, h->n_q_heads, &qo)))
     return nullptr;
-  const double theta = PyFloat_AsDouble(a[8]);
-  if (theta == -1.0 && PyErr_Occurred()) return nullptr;
+  float theta;
+  if (!number(a[8], "rope_theta", &theta)) return nullptr;
   if (given(a[9]) && !ints(*h, a[9], "rope_shift", {bt.n_seqs}, &shift)) return nullptr;
   return call(*h, n_rows, [&](dllm_stream s) {
     return h->append(&h->kv, &bt, has_q ? h->n_q_heads : 0, has_q ? &q : nullptr, &k, &v,
-                     has_q ? &qo : nullptr, pos, shift, (float)theta,
+                     has_q ? &qo : nullptr, pos, shift, theta,
                      static_cast<int32_t*>(h->ws), s);
   });
 }
@@ -203,12 +214,12 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !rows(*h, a[7], "out", n_rows, h->n_q_heads, &out) ||
       (given(a[8]) && !plain(*h, a[8], "lse", at::kFloat, {n_rows, h->n_q_heads}, &lse)))
     return nullptr;
-  const double scale = PyFloat_AsDouble(a[6]);
-  if (scale == -1.0 && PyErr_Occurred()) return nullptr;
+  float scale;
+  if (!number(a[6], "scale", &scale)) return nullptr;
   float* lp = static_cast<float*>(const_cast<void*>(lse));
   if (!given(a[9]))
     return call(*h, n_rows, [&](dllm_stream s) {
-      return h->attn(&h->kv, &bt, h->n_q_heads, segs, limit, (float)scale, &q, &out, lp, h->ws,
+      return h->attn(&h->kv, &bt, h->n_q_heads, segs, limit, scale, &q, &out, lp, h->ws,
                      h->ws_bytes, s);
     });
   const at::Tensor *gt = tensor(a[9], "group_start"), *pt = gt ? tensor(a[10], "prefix_table") : gt;
@@ -226,7 +237,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !ints(*h, a[11], "prefix_len", {groups}, &g.len))
     return nullptr;
   return call(*h, n_rows, [&](dllm_stream s) {
-    return h->shared(&h->kv, &bt, &g, h->n_q_heads, segs, limit, (float)scale, &q, &out, lp, h->ws,
+    return h->shared(&h->kv, &bt, &g, h->n_q_heads, segs, limit, scale, &q, &out, lp, h->ws,
                      h->ws_bytes, s);
   });
 }

@@ -56,6 +56,9 @@ class PagedKV:
             raise ValueError("the pages have to be on a GPU")
         if k_pages.stride(3) != 1:
             raise ValueError("the D elements of a head have to be contiguous")
+        for name, x in (("n_q_heads", n_q_heads), ("max_rows", max_rows), ("max_groups", max_groups)):
+            if not 0 <= x < 2 ** 31:
+                raise ValueError(f"{name}: {x} does not fit")
         self.k_pages, self.v_pages = k_pages, v_pages
         self.device, self.dtype = k_pages.device, k_pages.dtype
         n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_pages.shape
@@ -90,7 +93,8 @@ class PagedKV:
         rotated (into q_out, which may be q), or None without q.
 
         Rows [row_start[s], row_start[s+1]) go to positions pos[s].. of sequence s, rotated by
-        position + rope_shift[s]; page_table [n_seqs][pages] lists each sequence's pages."""
+        position + rope_shift[s]; page_table [n_seqs][pages] lists each sequence's pages.
+        rope_theta (0: no rotation) is taken in fp32, as the model configuration holds it."""
         if q is not None:
             if q_out is None:
                 q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -116,8 +120,8 @@ class PagedKV:
         receives each row's log-sum-exp.
 
         segs int32 [n_seqs][2][2]: (start, length) of the positions a sequence's rows see;
-        row_limit int32 [rows]: a row sees only positions below it.  Rows of no sequence are
-        left as they were (undefined in a fresh out)."""
+        row_limit int32 [rows]: a row sees only positions below it.  scale 0: 1 / sqrt(D).  Rows
+        of no sequence are left as they were (undefined in a fresh out)."""
         if out is None:
             out = self._out(q)
         status = self._attn(self._h, q, row_start, page_table, segs, row_limit, scale, out, lse,

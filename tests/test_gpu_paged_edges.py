@@ -349,3 +349,24 @@ def test_a_call_without_rows_does_nothing():
               lambda: kv.attn(q[:0], rs, a[1], a[2], row_limit=ints([1]))):
         with pytest.raises(ValueError):
             f()
+
+
+def test_numbers_that_do_not_fit_are_refused():
+    """Not cut to 32 bits, nor rounded to the zero that stands for the default."""
+    from diffusion_decoding_step_b200.paged import PagedKV
+    pool, kv, q, a = small()
+    for f in (lambda: PagedKV(*pool, 2 ** 32 + 4, 3), lambda: PagedKV(*pool, 4, 2 ** 32 + 3),
+              lambda: PagedKV(*pool, 4, 3, 2 ** 32 + 1), lambda: PagedKV(*pool, 4, 3, -1),
+              lambda: PagedKV(*pool, 4, 2 ** 31)):
+        with pytest.raises(ValueError, match="n_q_heads|max_rows|max_groups"):
+            f()
+    k, pos = torch.zeros(3, 2, 64, dtype=BF, device=DEV), ints([0, 0])
+    for tiny in (1e-46, 1e-300):
+        with pytest.raises(ValueError, match="scale"):
+            kv.attn(q, *a, scale=tiny)
+        with pytest.raises(ValueError, match="scale"):
+            kv.shared_prefix_attn(q, *a, ints([0, 2]), ints([[3]]), ints([9]), scale=tiny)
+        with pytest.raises(ValueError, match="rope_theta"):
+            kv.append(k, k, a[0], a[1], pos, rope_theta=tiny)
+    kv.attn(q, *a, scale=1e-40)
+    assert kv.device_status() == 0
