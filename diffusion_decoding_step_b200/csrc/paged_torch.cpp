@@ -5,6 +5,7 @@
 // The library's functions come as addresses, so that this module needs no
 // particular library file.
 #include <Python.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -15,6 +16,7 @@ namespace {
 
 struct Handle {
   dllm_kv_pages kv;
+  at::Tensor k_pages, v_pages;
   int n_q_heads, max_rows, max_groups, index;
   at::ScalarType type;
   void* ws;
@@ -43,6 +45,21 @@ bool refuse(const at::Tensor& t, const char* what, const char* needed) {
   PyErr_Format(PyExc_ValueError, "%s: %s is needed, got %s [%s] on %s", what, needed,
                c10::toString(t.scalar_type()), shape.c_str(), t.device().str().c_str());
   return false;
+}
+
+// The operators have no backward: a tensor whose gradient autograd would expect is refused.
+bool no_grad(const at::Tensor& t, const char* what) {
+  if (!t.requires_grad() || !at::GradMode::is_enabled()) return true;
+  PyErr_Format(PyExc_ValueError,
+               "%s requires a gradient, and the paged cache has no backward: call it under "
+               "torch.no_grad()",
+               what);
+  return false;
+}
+
+// Tells autograd that a tensor is written (inference tensors have no version).
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 // A contiguous tensor of `type` on the pages' GPU with the given extents (-1: any).
@@ -75,7 +92,8 @@ bool ints(const Handle& h, PyObject* o, const char* what, std::initializer_list<
   return true;
 }
 
-// Rows [n_rows][heads][D] of the pages' type with contiguous heads.
+// Rows [n_rows][heads][D] of the pages' type with contiguous heads; OUT: that are written.
+template <bool OUT = false>
 bool rows(const Handle& h, PyObject* o, const char* what, int64_t n_rows, int64_t heads,
           dllm_rows* out) {
   const at::Tensor* t = tensor(o, what);
@@ -89,7 +107,9 @@ bool rows(const Handle& h, PyObject* o, const char* what, int64_t n_rows, int64_
                    std::to_string(h.kv.head_dim) + "] on cuda:" + std::to_string(h.index) +
                    " with contiguous heads")
                       .c_str());
-  *out = dllm_rows{const_cast<void*>(t->const_data_ptr()), t->stride(0), t->stride(1)};
+  if (!no_grad(*t, what)) return false;
+  void* data = OUT ? t->mutable_data_ptr() : const_cast<void*>(t->const_data_ptr());
+  *out = dllm_rows{data, t->stride(0), t->stride(1)};
   return true;
 }
 
@@ -142,9 +162,11 @@ bool number(PyObject* o, const char* what, float* out) {
 }
 
 // create(pages struct address, n_q_heads, max_rows, max_groups, device, is_f16, ws, ws_bytes,
-//        append, attn, shared)
+//        append, attn, shared, k_pages, v_pages)
 PyObject* create(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 11) return PyErr_Format(PyExc_TypeError, "create: 11 arguments");
+  if (n != 13) return PyErr_Format(PyExc_TypeError, "create: 13 arguments");
+  const at::Tensor *kp = tensor(a[11], "k_pages"), *vp = kp ? tensor(a[12], "v_pages") : kp;
+  if (!vp) return nullptr;
   long long v[11];
   for (int i = 0; i < 11; ++i) {
     v[i] = PyLong_AsLongLong(a[i]);
@@ -152,6 +174,8 @@ PyObject* create(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   Handle* h = new Handle;
   h->kv = *reinterpret_cast<const dllm_kv_pages*>(v[0]);
+  h->k_pages = *kp;
+  h->v_pages = *vp;
   h->n_q_heads = (int)v[1];
   h->max_rows = (int)v[2];
   h->max_groups = (int)v[3];
@@ -181,11 +205,16 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   const bool has_q = given(a[6]);
   if (has_q && (!rows(*h, a[6], "q", n_rows, h->n_q_heads, &q) ||
-                !rows(*h, a[7], "q_out", n_rows, h->n_q_heads, &qo)))
+                !rows<true>(*h, a[7], "q_out", n_rows, h->n_q_heads, &qo)))
     return nullptr;
   float theta;
   if (!number(a[8], "rope_theta", &theta)) return nullptr;
   if (given(a[9]) && !ints(*h, a[9], "rope_shift", {bt.n_seqs}, &shift)) return nullptr;
+  if (n_rows > 0) {
+    written(h->k_pages);
+    written(h->v_pages);
+    if (has_q) written(*tensor(a[7], "q_out"));
+  }
   return call(*h, n_rows, [&](dllm_stream s) {
     return h->append(&h->kv, &bt, has_q ? h->n_q_heads : 0, has_q ? &q : nullptr, &k, &v,
                      has_q ? &qo : nullptr, pos, shift, theta,
@@ -211,17 +240,26 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!batch(*h, a[2], a[3], n_rows, &bt) || !rows(*h, a[1], "q", n_rows, h->n_q_heads, &q) ||
       !ints(*h, a[4], "segs", {bt.n_seqs, 2, 2}, &segs) ||
       (given(a[5]) && !ints(*h, a[5], "row_limit", {n_rows}, &limit)) ||
-      !rows(*h, a[7], "out", n_rows, h->n_q_heads, &out) ||
+      !rows<true>(*h, a[7], "out", n_rows, h->n_q_heads, &out) ||
       (given(a[8]) && !plain(*h, a[8], "lse", at::kFloat, {n_rows, h->n_q_heads}, &lse)))
     return nullptr;
+  const at::Tensor* lse_t = given(a[8]) ? tensor(a[8], "lse") : nullptr;
+  if (lse_t && !no_grad(*lse_t, "lse")) return nullptr;
   float scale;
   if (!number(a[6], "scale", &scale)) return nullptr;
-  float* lp = static_cast<float*>(const_cast<void*>(lse));
-  if (!given(a[9]))
+  float* lp = lse_t ? static_cast<float*>(lse_t->mutable_data_ptr()) : nullptr;
+  auto outputs_written = [&]() {
+    if (n_rows == 0) return;
+    written(*tensor(a[7], "out"));
+    if (lse_t) written(*lse_t);
+  };
+  if (!given(a[9])) {
+    outputs_written();
     return call(*h, n_rows, [&](dllm_stream s) {
       return h->attn(&h->kv, &bt, h->n_q_heads, segs, limit, scale, &q, &out, lp, h->ws,
                      h->ws_bytes, s);
     });
+  }
   const at::Tensor *gt = tensor(a[9], "group_start"), *pt = gt ? tensor(a[10], "prefix_table") : gt;
   if (!pt) return nullptr;
   const int64_t groups = gt->numel() - 1, width = pt->dim() == 2 ? pt->size(1) : -1;
@@ -236,6 +274,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !ints(*h, a[10], "prefix_table", {groups, -1}, &g.page_table) ||
       !ints(*h, a[11], "prefix_len", {groups}, &g.len))
     return nullptr;
+  outputs_written();
   return call(*h, n_rows, [&](dllm_stream s) {
     return h->shared(&h->kv, &bt, &g, h->n_q_heads, segs, limit, scale, &q, &out, lp, h->ws,
                      h->ws_bytes, s);

@@ -36,6 +36,9 @@ class PagedKV:
     call and sizes the workspace; ``max_groups`` bounds the prefix groups (0: no
     ``shared_prefix_attn``; the default is the most that a call takes).
 
+    The cache only serves, there is no backward: tensors that require a gradient are refused
+    while gradients are recorded (``torch.no_grad()``).
+
     Calls run on the current stream of the pages' device and return without waiting; a call
     without rows checks its arguments and does nothing.  The
     attention calls share one workspace: a PagedKV serves one of them at a time, and graphs or
@@ -54,6 +57,8 @@ class PagedKV:
             raise ValueError(f"pages of {k_pages.dtype}: bfloat16 or float16 is needed")
         if not k_pages.is_cuda:
             raise ValueError("the pages have to be on a GPU")
+        if k_pages.requires_grad or v_pages.requires_grad:
+            raise ValueError("the pages are written in place: they cannot require a gradient")
         if k_pages.stride(3) != 1:
             raise ValueError("the D elements of a head have to be contiguous")
         for name, x in (("n_q_heads", n_q_heads), ("max_rows", max_rows), ("max_groups", max_groups)):
@@ -82,7 +87,7 @@ class PagedKV:
         self._append, self._attn = binding.append, binding.attn
         self._h = binding.create(C.addressof(kv), n_q_heads, max_rows, max_groups,
                                  self.device.index, int(self.dtype is torch.float16),
-                                 self.ws.data_ptr(), n.value, *fns)
+                                 self.ws.data_ptr(), n.value, *fns, k_pages, v_pages)
 
     # ------------------------------------------------------------------ calls
     def append(self, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,

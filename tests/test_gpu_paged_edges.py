@@ -370,3 +370,48 @@ def test_numbers_that_do_not_fit_are_refused():
             kv.append(k, k, a[0], a[1], pos, rope_theta=tiny)
     kv.attn(q, *a, scale=1e-40)
     assert kv.device_status() == 0
+
+
+def test_no_gradients_are_dropped_in_silence():
+    pool, kv, q, a = small()
+    k, pos, out = torch.ones(3, 2, 64, dtype=BF, device=DEV), ints([0, 3]), torch.zeros_like(q)
+    qg, kg = q.clone().requires_grad_(), k.clone().requires_grad_()
+    calls = [lambda: kv.attn(qg, *a), lambda: kv.attn(q, *a, out=qg.clone()),
+             lambda: kv.shared_prefix_attn(qg, *a, ints([0, 2]), ints([[3]]), ints([9])),
+             lambda: kv.append(kg, k, a[0], a[1], pos), lambda: kv.append(k, kg * 2, a[0], a[1], pos),
+             lambda: kv.append(k, k, a[0], a[1], pos, q=qg, q_out=out)]
+    for f in calls:
+        with pytest.raises(ValueError, match="no backward"):
+            f()
+        with torch.no_grad():
+            f()
+    with torch.inference_mode():
+        kv.attn(qg, *a)
+    from diffusion_decoding_step_b200.paged import PagedKV
+    with pytest.raises(ValueError, match="gradient"):
+        PagedKV(pool[0].clone().requires_grad_(), pool[1].clone().requires_grad_(), 4, 3)
+
+
+def test_autograd_sees_what_a_call_has_written():
+    """Tensors that a backward pass has saved and that a call overwrites are refused there."""
+    pool, kv, q, a = small()
+    k, pos = torch.ones(3, 2, 64, dtype=BF, device=DEV), ints([0, 3])
+    out, lse, q_out = torch.ones_like(q), torch.ones(3, 4, device=DEV), torch.ones_like(q)
+    writes = [(pool[0], lambda: kv.append(k, k, a[0], a[1], pos)), (pool[1], lambda: kv.append(k, k, a[0], a[1], pos)),
+              (q_out, lambda: kv.append(k, k, a[0], a[1], pos, q=q, q_out=q_out)),
+              (out, lambda: kv.attn(q, *a, out=out, lse=lse)), (lse, lambda: kv.attn(q, *a, out=out, lse=lse))]
+    for x, f in writes:
+        w = torch.ones_like(x, requires_grad=True)
+        y = (x * w).float().sum()
+        f()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    y = (q * torch.ones_like(q, requires_grad=True)).float().sum()
+    kv.attn(q, *a)
+    y.backward()            # what is only read is as it was
+    y = (pool[0] * torch.ones_like(pool[0], requires_grad=True)).float().sum()
+    kv.append(k[:0], k[:0], ints([0, 0, 0]), a[1], pos)
+    y.backward()            # and so is everything after a call without rows
+    with torch.inference_mode():
+        o = torch.zeros_like(q)
+        kv.attn(q, *a, out=o)       # tensors without a version counter
