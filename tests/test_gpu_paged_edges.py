@@ -415,3 +415,128 @@ def test_autograd_sees_what_a_call_has_written():
     with torch.inference_mode():
         o = torch.zeros_like(q)
         kv.attn(q, *a, out=o)       # tensors without a version counter
+
+
+# ------------------------------------------------------------------ bounds
+class Guarded:
+    """Tensors inside one buffer of a byte pattern, 64 KiB and more between them."""
+    GAP, PATTERN = 65536, 0xA5
+
+    def __init__(self, total):
+        self.buf = torch.full((total,), self.PATTERN, dtype=torch.uint8, device=DEV)
+        self.at, self.parts = self.GAP, []
+
+    def put(self, x):
+        n = x.numel() * x.element_size()
+        view = self.buf[self.at:self.at + n].view(x.dtype).view(x.shape)
+        view.copy_(x)
+        self.parts.append((self.at, self.at + n))
+        self.at = (self.at + n + self.GAP + 1023) // 1024 * 1024
+        assert self.at <= self.buf.numel()
+        return view
+
+    def check(self):
+        edge = 0
+        for a, b in self.parts + [(self.buf.numel(), 0)]:
+            assert bool((self.buf[edge:a] == self.PATTERN).all()), f"written between bytes {edge} and {a}"
+            edge = b
+
+
+def steps_up(v, hi):
+    """What the kernels make of starts that may hold anything: clamped, then non-decreasing."""
+    out = []
+    for x in v:
+        out.append(max([min(max(x, 0), hi)] + out[-1:]))
+    return out
+
+
+WILD = [[-5, 3, 100], [8, 4, 0], [2 ** 31 - 1, LOW, 2 ** 31 - 1], [0, 8, 8], [5, 5, 6], [LOW, LOW, 7], [3, 0, 6]]
+
+
+@pytest.mark.parametrize("hq,hkv,D,dtype", [(2, 1, 64, BF), (28, 4, 128, HF), (6, 6, 32, BF)])
+def test_attention_with_any_starts_writes_only_its_outputs(hq, hkv, D, dtype):
+    """Any contents of row_start and group_start: nothing but out, lse and the workspace changes,
+    and the rows are those of the starts made non-decreasing."""
+    import ctypes as C
+
+    from diffusion_decoding_step_b200 import abi
+    from tests.gpu_util import ptr, stream
+    g = _gen(11)
+    n = 8
+    pool = make_pool(g, 12, hkv, 16, D, dtype, "heads")
+    table, ptab = torch.tensor([[0, 1, 9], [2, 3, 10]], dtype=torch.int32), torch.tensor([[4], [5]], dtype=torch.int32)
+    segs, plen = whole(40, 32), [9, -4]
+    gd = Guarded(64 << 20)
+    k, v = gd.put(pool[0]), gd.put(pool[1])
+    kept = [k.clone(), v.clone()]
+    q = gd.put(torch.randn(n, hq, D, generator=g).to(dtype).to(DEV))
+    out, lse = gd.put(torch.full_like(q, 7.0)), gd.put(torch.full((n, hq), 5.0, device=DEV))
+    t, pt, sg, pl = (gd.put(x.to(DEV)) for x in (table, ptab, ints(segs), ints(plen)))
+    rs, gs = gd.put(ints([0] * 3)), gd.put(ints([0] * 3))
+    a, b, qr, orow = c_call((k, v), q, out, rs, t)
+    size = C.c_size_t(0)
+    abi.check(abi.dllm_paged_workspace_size(a, hq, n, C.byref(size)), "size")
+    ws = gd.put(torch.zeros(size.value, dtype=torch.uint8, device=DEV))
+    grp = abi.dllm_prefix_groups(2, 1, pt.stride(0), gs.data_ptr(), pt.data_ptr(), pl.data_ptr())
+    abi.check(abi.dllm_paged_workspace_init(ptr(ws), size.value, stream()), "init")
+    pages = R.Pages(*[x.cpu().to(R.F64) for x in kept])
+
+    def one(starts, groups):
+        out.fill_(7.0), lse.fill_(5.0), rs.copy_(ints(starts))
+        if groups is None:
+            abi.check(abi.dllm_paged_attn(a, b, hq, ptr(sg), None, 0.0, qr, orow, ptr(lse), ptr(ws), size.value,
+                                          stream()), "attn")
+        else:
+            gs.copy_(ints(groups))
+            abi.check(abi.dllm_shared_prefix_attn(a, b, C.byref(grp), hq, ptr(sg), None, 0.0, qr, orow, ptr(lse),
+                                                  ptr(ws), size.value, stream()), "shared")
+        up = steps_up(starts, n)
+        ref = R.attention(pages, q.cpu(), up, table, segs, dtype=dtype,
+                          groups=None if groups is None else (steps_up(groups, 2), ptab, plen))
+        check_rows(out, ref, lse, torch.full_like(out, 7.0))
+        gd.check()
+        assert torch.equal(k, kept[0]) and torch.equal(v, kept[1])
+
+    for starts in WILD:
+        one(starts, None)
+        for groups in ([0, 1, 2], [-4, 7, 1], [2 ** 31 - 1, LOW, 5], [1, 0, 2]):
+            one(starts, groups)
+    code = C.c_int32(0)
+    abi.check(abi.dllm_device_status(ptr(ws), C.byref(code), stream()), "status")
+    assert code.value == 0
+
+
+@pytest.mark.parametrize("hq,hkv,D,dtype", [(2, 1, 64, BF), (28, 4, 128, HF)])
+def test_append_with_any_starts_writes_only_its_outputs(hq, hkv, D, dtype):
+    """Any contents of row_start, pos and the table: nothing outside the pages and q_out changes,
+    and the pages only in slots that a table row reaches."""
+    import ctypes as C
+
+    from diffusion_decoding_step_b200 import abi
+    from tests.gpu_util import ptr, stream
+    g = _gen(12)
+    n = 8
+    gd = Guarded(32 << 20)
+    pool = [gd.put(x) for x in make_pool(g, 6, hkv, 16, D, dtype, "heads")]
+    rows = [gd.put(torch.randn(n, h, D, generator=g).to(dtype).to(DEV)) for h in (hq, hkv, hkv)]
+    q_out = gd.put(torch.zeros(n, hq, D, dtype=dtype, device=DEV))
+    kept = [x.clone() for x in pool]
+    rs, pos, t = gd.put(ints([0] * 3)), gd.put(ints([0] * 2)), gd.put(ints([[0, 1], [2, 3]]))
+    status = gd.put(ints([0]))
+    a, b, q, o = c_call(pool, rows[0], q_out, rs, t)
+    k, v = (C.byref(abi.dllm_rows(x.data_ptr(), x.stride(0), x.stride(1))) for x in rows[1:])
+    for table in ([[0, 1], [2, 3]], [[-1, 6], [2 ** 31 - 1, LOW]], [[0, 99], [-7, 3]]):
+        for starts in WILD:
+            for where in ([0, 0], [15, 30], [LOW, 2 ** 31 - 1], [-3, 29]):
+                rs.copy_(ints(starts)), pos.copy_(ints(where)), t.copy_(ints(table))
+                abi.check(abi.dllm_paged_append(a, b, hq, q, k, v, o, ptr(pos), None, 1e4, ptr(status), stream()),
+                          "append")
+    gd.check()
+    for x, y in zip(pool, kept):
+        assert torch.equal(x[4:], y[4:])        # pages that no table row names
+
+
+def test_workspaces_and_tables_may_be_larger():
+    for c in (SHARED[0], SHARED[1], SHARED[8]):
+        run_attn(*c[:8], groups=c[8], kv_rows=5000, width=40)
+        run_attn(*c[:8], kv_rows=700, width=25)
