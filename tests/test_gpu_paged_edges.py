@@ -540,3 +540,56 @@ def test_workspaces_and_tables_may_be_larger():
     for c in (SHARED[0], SHARED[1], SHARED[8]):
         run_attn(*c[:8], groups=c[8], kv_rows=5000, width=40)
         run_attn(*c[:8], kv_rows=700, width=25)
+
+
+# ------------------------------------------------------------------ as they are used
+def test_growth_over_steps_matches_the_contiguous_cache():
+    """Two prompts of different lengths enter, then each sequence grows by three blocks: after
+    every append the attention gives what dllm_block_attn gives over the same keys."""
+    import ctypes as C
+
+    from diffusion_decoding_step_b200 import abi
+    from diffusion_decoding_step_b200 import workload as wl
+    from diffusion_decoding_step_b200.runtime import make_config, workspace_bytes
+    from tests.gpu_util import ptr, stream
+    g = _gen(41)
+    hq, hkv, D, ps, B, steps, prompts = 28, 4, 128, 16, 32, 3, [200, 57]
+    ends = [p + steps * B for p in prompts]
+    pool = make_pool(g, 60, hkv, ps, D, BF, "slots")
+    table, _ = make_tables(ends, ps, torch.randperm(60, generator=g).to(torch.int32))
+    tab = table.to(DEV)
+    kv = make_kv(pool, hq, sum(prompts))
+    w = wl.Workload("t", batch=2, n_layers=1, hidden=512, n_q_heads=hq, n_kv_heads=hkv, head_dim=D, vocab=1024,
+                    prompt_len=224, gen_len=steps * B, block=B)
+    cfg, size = make_config(w), workspace_bytes(w)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    abi.check(abi.dllm_workspace_init(C.byref(cfg), ptr(ws), size, stream()), "ws init")
+    kc = torch.zeros(1, 2, hkv, w.seq_len, D, dtype=BF, device=DEV)
+    vc = torch.zeros_like(kc)
+
+    def rows(n):
+        x = torch.randn(n, hq + 2 * hkv, D, generator=g).to(BF).to(DEV)
+        return x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+
+    _, k, v = rows(sum(prompts))
+    kv.append(k, v, ints([0, prompts[0], sum(prompts)]), tab, ints([0, 0]), rope_theta=1e6)
+    rs = [0, B, 2 * B]
+    for step in range(steps):
+        at = [p + step * B for p in prompts]
+        lens = [n + B for n in at]
+        q, k, v = rows(2 * B)
+        q = kv.append(k, v, ints(rs), tab, ints(at), q=q, rope_theta=1e6)
+        out = kv.attn(q, ints(rs), tab, ints(whole(*lens)))
+        pages = host(pool)
+        for s in range(2):      # the same keys in the contiguous cache
+            for cache, x in zip((kc, vc), pages.gather(table[s], torch.arange(lens[s]))):
+                cache[0, s, :, :lens[s]] = x.to(BF).to(DEV)
+        qb = q.reshape(2, B, hq, D).transpose(1, 2).contiguous()
+        want = torch.empty(2 * B, hq * D, dtype=BF, device=DEV)
+        abi.check(abi.dllm_block_attn(C.byref(cfg), 0, B, ptr(qb), ptr(kc), ptr(vc), ptr(ints(whole(*lens))), ptr(want),
+                                      ptr(ws), size, stream()), "attn")
+        torch.cuda.synchronize()
+        ref = R.attention(pages, q.cpu(), rs, table, whole(*lens))
+        check_rows(out, ref)
+        check_rows(want.reshape(2 * B, hq, D), ref)
+    assert kv.device_status() == 0
