@@ -279,13 +279,17 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 // rounded to the cache's type for the second product (half a step each, as its
 // input type demands), the sum takes it unrounded.
 //
-// What bounds it, measured: few query rows by the keys' bytes (a token each of 32
-// sequences, 28 heads over 4, 281 MB: 57 us, 4.9 TB/s; one token over 131,001 keys
-// 54.5 us, the same rate; blocks of 32 rows of 16 sequences, 32 heads, 284 MB: 60 us,
-// 4.7 TB/s; in the steady state 6 TB/s, the rest is the start and the merge); many
-// by the products and the softmax between them (32 blocks of 32 rows that share 8192
-// keys 135 us, 920 TFLOP/s; two chunks of 1024 rows at 2 to 4 thousand keys 90 us,
-// 630); short ones by latency (32 rows over 544 keys 14 us).
+// What bounds it, measured over twelve calls captured in a graph, on three inputs in
+// turn (called one by one they take up to 6 us more, the longest 154 instead of 135):
+// few query rows by the keys' bytes (a token each of 32 sequences, 28 heads over 4,
+// 281 MB: 57 us, 4.9 TB/s; one token over 131,001 keys 54 us, the same rate; blocks of
+// 32 rows of 16 sequences, 32 heads, 284 MB: 60 us, 4.7 TB/s; in the steady state 6
+// TB/s, the rest is the start and the merge); many by the products and the softmax
+// between them (32 blocks of 32 rows that share 8192 keys 135 us, 920 TFLOP/s) and by
+// uneven shares under a limit (two chunks of 1024 rows at 2 to 4 thousand keys 86 us,
+// 665 TFLOP/s: a query tile is allotted all keys of its sequence); short ones by
+// latency (32 rows over 544 keys 14 us).  Figures of single steps below are from
+// before and after that step.
 //
 // All query tiles of all items and kv heads, each with its key tiles plus a
 // fixed cost, form one line that the CTAs (one per SM) cut into equal shares,
@@ -320,8 +324,8 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 // Query tiles and streams:
 //   kSplit  128 rows; the streams take key tiles in turn and are merged at the
 //           end of a piece.  (256 rows, a half for each stream, share K and V but
-//           halve the number of tiles to spread: 32 rows over 544 keys 15.9 us
-//           instead of 14.0, 32 blocks 144 instead of 140, the prompt chunks 87
+//           halve the number of tiles to spread.  Measured when 32 blocks took 140 us:
+//           144; 32 rows over 544 keys 15.9 us instead of 14.0, the prompt chunks 87
 //           instead of 90.)
 //   kQuad   32 rows, in four copies on the 128 lanes of TMEM; the streams take key
 //           tiles in turn, and warp w of a stream takes the w-th quarter
