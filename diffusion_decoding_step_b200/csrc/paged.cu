@@ -1430,7 +1430,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (v == 0.f) continue;
           if (whole)
             out[col - c0] = (uint16_t)pack2<F16>(v, 0.f);
-          else if (lt != 0.f)
+          else
             reinterpret_cast<float*>(part + col / 4 * p.slot_rows)[col & 3] = v;
         }
       };
@@ -1504,7 +1504,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 *reinterpret_cast<uint4*>(out + col) = make_uint4(u[0], u[1], u[2], u[3]);
               else
                 *reinterpret_cast<uint2*>(out + col) = make_uint2(u[0], u[1]);
-            } else if (lt != 0.f) {
+            } else if (d.n > 0) {
 #pragma unroll
               for (int i = 0; i < kOwn; i += 4)
                 part[(c0 + col + i) / 4 * p.slot_rows] =
@@ -1534,7 +1534,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (some0) add(at, a0);
           if (some1) add(at + 128, a1);
           if (!whole) {
-            if (valid && lt != 0.f) {
+            if (valid && d.n > 0) {
 #pragma unroll
               for (int i = 0; i < kC; i += 4)
                 part[(c0 + c * kC + i) / 4 * p.slot_rows] =
@@ -1574,7 +1574,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (valid && (warp == 0 || (!QUAD && wg == 0))) {
         if (!whole)
-          p.part_ml[(size_t)d.slot * p.slot_rows + qrow] = make_float2(mt, lt);
+          p.part_ml[(size_t)d.slot * p.slot_rows + qrow] = make_float2(mt, d.n > 0 ? lt : -1.f);
         else if (p.lse != nullptr)
           p.lse[(size_t)r * p.Hq + head] = log_sum(mt, lt);
       }
@@ -1630,7 +1630,7 @@ constexpr int kMergeWarps = 8, kMergeBlocks = 4 * kNumSMs;
 struct RowSum {
   float m = -FLT_MAX, l = 0.f, o[8] = {};
   DLLM_DEV void join(float2 ml, const float4& x, const float4& y) {
-    if (ml.y == 0.f) return;  // a part without keys, whose elements are not written
+    if (ml.y < 0.f) return;  // a part without key tiles, whose elements are not written
     const float mn = fmaxf(m, ml.x);
     const float a = fast_exp2(m - mn), b = fast_exp2(ml.x - mn);
     m = mn;
@@ -1689,7 +1689,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
 #pragma unroll
         for (int k = 0; k < kUn; ++k) {
           const int ip = i + k * split;
-          ml[k] = make_float2(-FLT_MAX, 0.f);
+          ml[k] = make_float2(-FLT_MAX, -1.f);
           if (ip < tile.z) {
             const size_t ro =
                 (size_t)(ip == 0 ? tile.w : (tile.w & ~1) + 2 * ip) * p.slot_rows;

@@ -224,6 +224,19 @@ def test_later_keys_do_not_spoil_earlier_rows(case, grouped):
                groups=([0, len(rows)], [150]) if grouped else None)
 
 
+@pytest.mark.parametrize("case", [
+    # a key of score minus infinity for some heads, alone in its part of a cut tile; its value counts in whole and
+    # in cut tiles alike
+    (BF, 64, 16, 8, 256, "heads", [2], whole(1), [(0, 0, "k", 53, INF), (0, 0, "v", 45, NAN)], ([0, 1], [1])),
+    (HF, 64, 8, 1, 1024, "heads", [1, 33], whole(300, 1), [(1, 0, "k", 46, -INF), (1, 0, "v", 56, -INF)], ([0, 2], [1])),
+    (HF, 128, 8, 8, 256, "padded", [1, 2], [((0, 129), (0, 0)), ((187, 1), (233, 1))],
+     [(1, 187, "k", 99, INF), (1, 187, "v", 27, NAN), (1, 187, "v", 107, INF)], None),
+    (BF, 128, 4, 1, 64, "slots", [1], whole(20000), [(0, p, w, 7, INF) for p in range(0, 20000, 64) for w in "kv"], None),
+], ids=lambda c: str(c)[:60])
+def test_values_of_keys_that_weigh_nothing_count(case):
+    run_spoilt(*case[:9], groups=case[9])
+
+
 # ------------------------------------------------------------------ waits that run out
 def c_call(pool, q, out, rs, table):
     """Argument blocks of the C calls over these tensors."""
