@@ -280,7 +280,7 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
 // input type demands), the sum takes it unrounded.
 //
 // What bounds it, measured over twelve calls captured in a graph, on three inputs in
-// turn (called one by one they take up to 6 us more, the longest 154 instead of 135):
+// turn (called one by one they take up to 6 us more, the longest 155 instead of 135 us):
 // few query rows by the keys' bytes (a token each of 32 sequences, 28 heads over 4,
 // 281 MB: 57 us, 4.9 TB/s; one token over 131,001 keys 54 us, the same rate; blocks of
 // 32 rows of 16 sequences, 32 heads, 284 MB: 60 us, 4.7 TB/s; in the steady state 6

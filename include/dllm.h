@@ -383,7 +383,7 @@ typedef struct {
 
 typedef struct {
   int32_t n_seqs, n_rows;     /* n_rows: rows of the row buffers */
-  int32_t max_pages;          /* entries of a table row that may be used */
+  int32_t max_pages;          /* entries of a table row that may be used, >= 1 */
   int32_t table_stride;       /* entries from one table row to the next, >= max_pages */
   const int32_t* row_start;   /* [n_seqs + 1] */
   const int32_t* page_table;  /* [n_seqs][table_stride] */
